@@ -23,9 +23,11 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 # tests point it at a host-only build instrumented with AddressSanitizer and UBSan).
 LIB_PATH = os.environ.get("MOE_LATENT_LIB") or os.path.join(_PKG, "libmoe_latent.so")
 
-# enum values of include/moe_latent.h
+# enum values of include/moe_latent.h and include/moe_drafted.h
 MOE_DT_BF16, MOE_DT_F16, MOE_DT_F32, MOE_DT_U32, MOE_DT_I32 = 1, 2, 3, 4, 5
 MOE_ACT_RELU2 = 1
+MOE_ROPE_HALF, MOE_ROPE_INTERLEAVED = 1, 2
+FLAG = {"page": 1, "len": 2, "rows": 4, "path": 8, "token": 16, "logits": 32}
 STATUS = {
     0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_TOPK_GT_EXPERTS", 3: "MOE_ERR_GROUPS",
     4: "MOE_ERR_SHAPE", 5: "MOE_ERR_MISSING_TENSOR", 6: "MOE_ERR_DTYPE", 7: "MOE_ERR_LAYOUT",
@@ -56,6 +58,16 @@ class moe_latent_weights(ctypes.Structure):
     _fields_ = [(n, moe_tensor) for n in WEIGHT_FIELDS]
 
 
+class moe_paged_cache(ctypes.Structure):
+    _fields_ = [("k", moe_tensor), ("v", moe_tensor), ("table", moe_tensor), ("len", moe_tensor),
+                ("flags", ctypes.c_void_p)]
+
+
+class moe_rope(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("pairs", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("magnitude", ctypes.c_float)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, code: int, message: str):
         super().__init__(f"{STATUS.get(code, code)}: {message}")
@@ -68,6 +80,7 @@ def _load():
         raise ImportError(f"{LIB_PATH} is not built (run __graft_entry__.build())")
     lib = ctypes.CDLL(LIB_PATH)
     P = ctypes.c_void_p
+    i32, i64 = ctypes.c_int32, ctypes.c_int64
     sig = {
         "moe_latent_create": (ctypes.c_int, [ctypes.POINTER(moe_latent_config),
                                              ctypes.POINTER(moe_latent_weights), P,
@@ -93,6 +106,15 @@ def _load():
         "moe_latent_forward_static": (ctypes.c_int, [ctypes.POINTER(moe_latent_config),
                                                      ctypes.POINTER(moe_latent_weights), ctypes.c_int32,
                                                      P, P, P]),
+        # include/moe_drafted.h
+        "moe_paged_cache_check": (ctypes.c_int, [P]),
+        "moe_rope_append": (ctypes.c_int, [P, P, i32, P, i64, i32, P, i64, P, i64, P, P, P, i64, P]),
+        "moe_tree_attend": (ctypes.c_int, [P, i32, P, i64, i32, P, P, ctypes.c_float, P, i64, P, ctypes.c_size_t, P]),
+        "moe_tree_attend_workspace": (i64, [P, i32, i32]),
+        "moe_draft_verify": (ctypes.c_int, [P, P, P, i32, P, P, P, P, i64, P, P, P, P, P, P, P, ctypes.c_size_t, P]),
+        "moe_draft_verify_workspace": (i64, [i32, i32, i32]),
+        "moe_path_keep": (ctypes.c_int, [P, P, i32, P, P, P, P]),
+        "moe_drafted_status": (ctypes.c_int, [P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -108,6 +130,9 @@ EXPORTED = ("moe_latent_create", "moe_latent_forward", "moe_latent_destroy", "mo
             "moe_latent_launch_group", "moe_latent_group_items", "moe_latent_forward_timed",
             "moe_latent_stream_read", "moe_latent_forward_static", "moe_latent_group_stages",
             "moe_lm_head_gemv", "moe_latent_prefill", "moe_latent_group_kernel")
+# the functions of include/moe_drafted.h (drafted.py calls them)
+DRAFTED = ("moe_paged_cache_check", "moe_rope_append", "moe_tree_attend", "moe_tree_attend_workspace",
+           "moe_draft_verify", "moe_draft_verify_workspace", "moe_path_keep", "moe_drafted_status")
 
 
 def lib():

@@ -12,7 +12,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmoe_latent.so")
-SOURCES = ["layer_kernels.hip", "prefill_kernels.hip", "moe_latent_api.hip"]
+SOURCES = ["layer_kernels.hip", "prefill_kernels.hip", "moe_latent_api.hip", "drafted_kernels.hip",
+           "attend_kernels.hip", "moe_drafted_api.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

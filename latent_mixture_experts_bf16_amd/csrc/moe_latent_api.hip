@@ -73,6 +73,20 @@ static int fail(int code, const char *fmt, ...) {
     return code;
 }
 
+namespace moe {
+// the same message for the drafted step's host file
+int api_fail(int code, const char *fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_err = buf;
+    return code;
+}
+void api_clear() { g_err.clear(); }
+}  // namespace moe
+
 // Device allocation with leak accounting. MOE_LATENT_FAIL_ALLOC_AT=n makes the n-th
 // allocation after the variable was set (or last changed) fail, to test the release paths.
 static std::mutex g_fail_mu;

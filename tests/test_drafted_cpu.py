@@ -1,0 +1,255 @@
+"""The drafted step's C ABI and its Python classes without a GPU: the library exports what
+include/moe_drafted.h declares, every bad argument is refused by name before a device is touched, and
+the host helpers (frequencies, masks) follow their definitions."""
+import ctypes
+import math
+import os
+import re
+
+import pytest
+import torch
+
+from latent_mixture_experts_bf16_amd import binding as B
+from latent_mixture_experts_bf16_amd import drafted as D
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 0x10000   # a non-NULL address; refused arguments are never dereferenced
+
+
+def test_library_exports_every_declared_function():
+    with open(os.path.join(ROOT, "include", "moe_drafted.h")) as f:
+        declared = sorted(set(re.findall(r"^\w[\w ]*\b(moe_\w+)\(", f.read(), re.M)))
+    assert declared == sorted(B.DRAFTED)
+    for name in declared:
+        assert hasattr(B.lib(), name), name
+
+
+def _cache(**over):
+    shape = over.pop("shape", [4, 16, 2, 64])
+    c = B.moe_paged_cache()
+    c.k = over.pop("k", B.make_tensor(FAKE, B.MOE_DT_BF16, shape))
+    c.v = over.pop("v", B.make_tensor(FAKE, B.MOE_DT_BF16, shape))
+    c.table = over.pop("table", B.make_tensor(FAKE, B.MOE_DT_I32, [3, 5]))
+    c.len = over.pop("len", B.make_tensor(FAKE, B.MOE_DT_I32, [3]))
+    c.flags = over.pop("flags", FAKE)
+    assert not over
+    return c
+
+
+def _says(rc, status, text):
+    assert B.STATUS[rc] == status, (B.STATUS[rc], B.moe_latent_last_error())
+    assert text in B.moe_latent_last_error(), B.moe_latent_last_error()
+
+
+T = B.make_tensor
+BF, F16, F32, I32 = B.MOE_DT_BF16, B.MOE_DT_F16, B.MOE_DT_F32, B.MOE_DT_I32
+
+
+@pytest.mark.parametrize("over,status,text", [
+    (dict(k=T(0, BF, [4, 16, 2, 64])), "MOE_ERR_MISSING_TENSOR", "cache k"),
+    (dict(k=T(FAKE, F32, [4, 16, 2, 64])), "MOE_ERR_DTYPE", "cache k"),
+    (dict(v=T(FAKE, F16, [4, 16, 2, 64])), "MOE_ERR_DTYPE", "cache v"),
+    (dict(k=T(FAKE, BF, [64, 2, 64])), "MOE_ERR_LAYOUT", "rank 3"),
+    (dict(shape=[4, 8, 2, 64]), "MOE_ERR_SHAPE", "page of 8"),
+    (dict(shape=[4, 24, 2, 64]), "MOE_ERR_SHAPE", "page of 24"),
+    (dict(shape=[4, 16, 2, 72]), "MOE_ERR_SHAPE", "head width 72"),
+    (dict(shape=[0, 16, 2, 64]), "MOE_ERR_SHAPE", "dim 0 is 0"),
+    (dict(v=T(FAKE, BF, [4, 16, 1, 64])), "MOE_ERR_SHAPE", "cache v: dim 2"),
+    (dict(k=T(FAKE + 2, BF, [4, 16, 2, 64])), "MOE_ERR_LAYOUT", "16-byte"),
+    (dict(k=T(FAKE, BF, [4, 16, 2, 64], [2048, 132, 64, 1])), "MOE_ERR_LAYOUT", "stride[1]"),
+    (dict(k=T(FAKE, BF, [4, 16, 2, 64], [2048, 128, 32, 1])), "MOE_ERR_LAYOUT", "overlap"),
+    (dict(k=T(FAKE, BF, [4, 16, 2, 64], [2048, 128, 1, 64])), "MOE_ERR_LAYOUT", "last dim"),
+    (dict(k=T(FAKE, BF, [4, 16, 2, 64], [1 << 34, 1 << 29, 64, 1])), "MOE_ERR_SHAPE", "2^30"),
+    (dict(table=T(FAKE, F32, [3, 5])), "MOE_ERR_DTYPE", "cache table"),
+    (dict(table=T(FAKE, I32, [15])), "MOE_ERR_LAYOUT", "cache table: rank"),
+    (dict(table=T(FAKE, I32, [3, 5], [1, 3])), "MOE_ERR_LAYOUT", "cache table"),
+    (dict(len=T(FAKE, I32, [2])), "MOE_ERR_SHAPE", "cache len: 2"),
+    (dict(len=T(0, I32, [3])), "MOE_ERR_MISSING_TENSOR", "cache len"),
+    (dict(flags=0), "MOE_ERR_INVALID_ARG", "flags"),
+])
+def test_cache_refusals(over, status, text):
+    c = _cache(**over)
+    _says(B.lib().moe_paged_cache_check(ctypes.byref(c)), status, text)
+    assert B.lib().moe_tree_attend_workspace(ctypes.byref(c), 1, 4) < 0
+
+
+def test_cache_descriptions_that_are_taken():
+    for shape in ([4, 16, 2, 64], [1, 48, 1, 80], [7, 256, 8, 256]):
+        assert B.lib().moe_paged_cache_check(ctypes.byref(_cache(shape=shape))) == 0
+    heads_first = T(FAKE, BF, [4, 16, 2, 64], [2048, 64, 1024, 1])
+    assert B.lib().moe_paged_cache_check(ctypes.byref(_cache(k=heads_first, v=heads_first))) == 0
+
+
+def _append(c=None, rope=None, rows=2, q=FAKE, qs=256, heads=4, k=FAKE + 0x10000, ks=128, v=FAKE + 0x20000, vs=128,
+            starts=FAKE, pos=None, out=FAKE + 0x30000, os_=256):
+    c = c or _cache()
+    rope = rope or B.moe_rope(FAKE, 32, B.MOE_ROPE_HALF, 1.0)
+    return B.lib().moe_rope_append(ctypes.byref(c), ctypes.byref(rope), rows, q, qs, heads, k, ks, v, vs, starts, pos, out,
+                                   os_, None)
+
+
+@pytest.mark.parametrize("over,status,text", [
+    (dict(rows=0), "MOE_ERR_ROWS", "rows 0"),
+    (dict(heads=3, qs=192, os_=192), "MOE_ERR_SHAPE", "3 heads"),
+    (dict(rope=B.moe_rope(0, 32, 1, 1.0)), "MOE_ERR_INVALID_ARG", "freqs"),
+    (dict(rope=B.moe_rope(FAKE, 33, 1, 1.0)), "MOE_ERR_SHAPE", "33 pairs"),
+    (dict(rope=B.moe_rope(FAKE, 0, 1, 1.0)), "MOE_ERR_SHAPE", "0 pairs"),
+    (dict(rope=B.moe_rope(FAKE, 32, 3, 1.0)), "MOE_ERR_INVALID_ARG", "layout 3"),
+    (dict(rope=B.moe_rope(FAKE, 32, 1, math.inf)), "MOE_ERR_INVALID_ARG", "magnitude"),
+    (dict(q=None), "MOE_ERR_INVALID_ARG", "q: NULL"),
+    (dict(qs=255), "MOE_ERR_LAYOUT", "q: row stride"),
+    (dict(k=FAKE + 1), "MOE_ERR_LAYOUT", "k: pointer"),
+    (dict(starts=None), "MOE_ERR_INVALID_ARG", "row_start"),
+    (dict(pos=FAKE + 2), "MOE_ERR_LAYOUT", "positions"),
+    (dict(out=FAKE + 2), "MOE_ERR_ALIAS", "q_out partially"),
+    (dict(out=FAKE, os_=264), "MOE_ERR_ALIAS", "q_out partially"),
+    (dict(out=FAKE + 0x10000), "MOE_ERR_ALIAS", "q_out overlaps k"),
+    (dict(rope=B.moe_rope(FAKE, 32, 2, 1.0), q=FAKE + 2), "MOE_ERR_LAYOUT", "interleaved"),
+])
+def test_append_refusals(over, status, text):
+    _says(_append(**over), status, text)
+
+
+def _attend(c=None, rows=2, q=FAKE, qs=256, heads=4, starts=FAKE, mask=None, scale=0.1, out=FAKE + 0x30000, os_=256):
+    c = c or _cache()
+    return B.lib().moe_tree_attend(ctypes.byref(c), rows, q, qs, heads, starts, mask, scale, out, os_, None, 0, None)
+
+
+@pytest.mark.parametrize("over,status,text", [
+    (dict(rows=(1 << 20) + 1), "MOE_ERR_ROWS", "rows"),
+    (dict(heads=5, qs=320, os_=320), "MOE_ERR_SHAPE", "5 heads"),
+    (dict(q=FAKE + 8), "MOE_ERR_LAYOUT", "q: pointer"),
+    (dict(qs=260), "MOE_ERR_LAYOUT", "q: pointer and row stride"),
+    (dict(os_=128), "MOE_ERR_LAYOUT", "out: row stride"),
+    (dict(mask=FAKE + 4), "MOE_ERR_LAYOUT", "mask"),
+    (dict(scale=math.nan), "MOE_ERR_INVALID_ARG", "scale"),
+    (dict(out=FAKE), "MOE_ERR_ALIAS", "out overlaps q"),
+    (dict(out=FAKE + 256), "MOE_ERR_ALIAS", "out overlaps q"),
+])
+def test_attend_refusals(over, status, text):
+    _says(_attend(**over), status, text)
+
+
+def _verify(z=None, tokens=FAKE, starts=FAKE, seqs=2, parent=None, ut=FAKE, up=FAKE, q=FAKE, qs=1000, temp=None,
+            n=FAKE, path=FAKE, said=FAKE, lp=FAKE, flags=FAKE, ws=FAKE, wsb=1 << 30):
+    z = z or T(FAKE, F32, [4, 1000])
+    return B.lib().moe_draft_verify(ctypes.byref(z), tokens, starts, seqs, parent, ut, up, q, qs, temp, n, path, said, lp,
+                                    flags, ws, wsb, None)
+
+
+@pytest.mark.parametrize("over,status,text", [
+    (dict(z=T(0, F32, [4, 1000])), "MOE_ERR_MISSING_TENSOR", "logits"),
+    (dict(z=T(FAKE, I32, [4, 1000])), "MOE_ERR_DTYPE", "logits"),
+    (dict(z=T(FAKE, F32, [4000])), "MOE_ERR_LAYOUT", "rank 1"),
+    (dict(z=T(FAKE, F32, [4, (1 << 20) + 1])), "MOE_ERR_SHAPE", "vocabulary"),
+    (dict(z=T(FAKE, F32, [0, 1000])), "MOE_ERR_ROWS", "rows 0"),
+    (dict(z=T(FAKE, F32, [4, 1000], [1, 4])), "MOE_ERR_LAYOUT", "strides"),
+    (dict(z=T(FAKE + 2, F32, [4, 1000])), "MOE_ERR_LAYOUT", "logits"),
+    (dict(seqs=0), "MOE_ERR_SHAPE", "sequences"),
+    (dict(tokens=None), "MOE_ERR_INVALID_ARG", "tokens"),
+    (dict(ut=None), "MOE_ERR_INVALID_ARG", "u_test"),
+    (dict(up=FAKE + 1), "MOE_ERR_LAYOUT", "u_pick"),
+    (dict(qs=999), "MOE_ERR_LAYOUT", "draft_probs"),
+    (dict(temp=FAKE + 2), "MOE_ERR_LAYOUT", "temperature"),
+    (dict(parent=FAKE + 2), "MOE_ERR_LAYOUT", "parent"),
+    (dict(flags=None), "MOE_ERR_INVALID_ARG", "flags"),
+])
+def test_verify_refusals(over, status, text):
+    _says(_verify(**over), status, text)
+
+
+def test_keep_refusals():
+    c = _cache()
+    call = lambda *a: B.lib().moe_path_keep(ctypes.byref(c), *a, None)  # noqa: E731
+    _says(call(FAKE, 0, FAKE, FAKE, FAKE), "MOE_ERR_ROWS", "rows")
+    _says(call(None, 4, FAKE, FAKE, FAKE), "MOE_ERR_INVALID_ARG", "row_start")
+    _says(call(FAKE, 4, FAKE + 1, FAKE, FAKE), "MOE_ERR_LAYOUT", "n_keep")
+    _says(call(FAKE, 4, FAKE, None, FAKE), "MOE_ERR_INVALID_ARG", "path")
+    _says(call(FAKE, 4, FAKE, FAKE, None), "MOE_ERR_INVALID_ARG", "new_len")
+    _says(B.lib().moe_drafted_status(None, None), "MOE_ERR_INVALID_ARG", "flags")
+
+
+# ------------------------------------------------------------------ the Python classes, on host tensors
+
+def _host_cache(dtype=torch.bfloat16):
+    k = torch.zeros(4, 16, 2, 64, dtype=dtype)
+    return D.PagedCache(k, torch.zeros_like(k), torch.zeros(3, 5, dtype=torch.int32), torch.zeros(3, dtype=torch.int32))
+
+
+def _refused(name, text, f, *a, **k):
+    with pytest.raises(B.MoeError) as e:
+        f(*a, **k)
+    assert e.value.name == name and text in str(e.value), str(e.value)
+
+
+def test_python_checks():
+    c = _host_cache()
+    q = torch.zeros(4, 256, dtype=torch.bfloat16)
+    kv = torch.zeros(4, 128, dtype=torch.bfloat16)
+    starts = torch.tensor([0, 1, 2, 4], dtype=torch.int32)
+    rope = D.Rope([1.0] * 32, device="cpu")
+    _refused("MOE_ERR_DEVICE", "GPU", c.append, rope, q, kv, kv, starts)
+    _refused("MOE_ERR_DEVICE", "GPU", c.attend, q, starts)
+    _refused("MOE_ERR_DTYPE", "q:", c.attend, q.float(), starts)
+    _refused("MOE_ERR_SHAPE", "not heads", c.attend, q[:, :100], starts)
+    _refused("MOE_ERR_LAYOUT", "rank 3", c.attend, q[None], starts)
+    _refused("MOE_ERR_LAYOUT", "columns", c.attend, torch.zeros(256, 4, dtype=torch.bfloat16).T, starts)
+    _refused("MOE_ERR_SHAPE", "row_start", c.attend, q, starts[:3])
+    _refused("MOE_ERR_DTYPE", "row_start", c.attend, q, starts.long())
+    _refused("MOE_ERR_DTYPE", "mask", c.attend, q, starts, mask=torch.zeros(4, dtype=torch.int32))
+    _refused("MOE_ERR_SHAPE", "mask", c.attend, q, starts, mask=torch.zeros(3, dtype=torch.int64))
+    _refused("MOE_ERR_SHAPE", "out", c.attend, q, starts, out=q[:2])
+    _refused("MOE_ERR_SHAPE", "k:", c.append, rope, q, kv[:3], kv, starts)
+    _refused("MOE_ERR_DTYPE", "positions", c.append, rope, q, kv, kv, starts, positions=torch.zeros(4))
+    _refused("MOE_ERR_LAYOUT", "positions", c.append, rope, q, kv, kv, starts,
+             positions=torch.zeros(8, dtype=torch.int32)[::2])
+    n = torch.ones(3, dtype=torch.int32)
+    _refused("MOE_ERR_DEVICE", "GPU", c.keep, starts, n, torch.zeros(4, dtype=torch.int32))
+    _refused("MOE_ERR_SHAPE", "n_keep", c.keep, starts, n[:2], torch.zeros(4, dtype=torch.int32))
+    _refused("MOE_ERR_SHAPE", "cache v", D.PagedCache, c.k, c.v[:, :, :1], c.table, c.length)
+    _refused("MOE_ERR_DTYPE", "cache k", D.PagedCache, c.k.float(), c.v.float(), c.table, c.length)
+    _refused("MOE_ERR_INVALID_ARG", "layout", D.Rope, [1.0], layout="other", device="cpu")
+    _refused("MOE_ERR_SHAPE", "freqs", D.Rope, [[1.0]], device="cpu")
+
+
+def test_python_checks_of_the_verifier():
+    v = D.Verifier(100, max_rows=4, max_seqs=2, device="cpu")
+    z, i, f = torch.zeros(4, 100), torch.zeros(4, dtype=torch.int32), torch.zeros(4)
+    starts = torch.tensor([0, 2, 4], dtype=torch.int32)
+    _refused("MOE_ERR_DEVICE", "GPU", v.verify, z, i, starts, f, f)
+    _refused("MOE_ERR_ROWS", "5 rows", v.verify, torch.zeros(5, 100), i, starts, f, f)
+    _refused("MOE_ERR_ROWS", "3 sequences", v.verify, z, i, torch.zeros(4, dtype=torch.int32), f, f)
+    _refused("MOE_ERR_SHAPE", "logits", v.verify, z[:, :99], i, starts, f, f)
+    _refused("MOE_ERR_DTYPE", "logits", v.verify, z.double(), i, starts, f, f)
+    _refused("MOE_ERR_DTYPE", "tokens", v.verify, z, i.long(), starts, f, f)
+    _refused("MOE_ERR_SHAPE", "u_pick", v.verify, z, i, starts, f, f[:3])
+    _refused("MOE_ERR_DTYPE", "draft_probs", v.verify, z, i, starts, f, f, draft_probs=z.bfloat16())
+    _refused("MOE_ERR_SHAPE", "temperature", v.verify, z, i, starts, f, f, temperature=f)
+    _refused("MOE_ERR_SHAPE", "vocabulary", D.Verifier, 0, 4, 2, device="cpu")
+
+
+def test_frequencies():
+    f, m = D.rope_frequencies(8)
+    assert m == 1.0 and torch.allclose(f, torch.tensor([1.0, 0.1, 0.01, 0.001], dtype=torch.float64), rtol=1e-14)
+    g, _ = D.rope_frequencies(8, scaling="linear", factor=4)
+    assert torch.equal(g, f / 4)
+    g, _ = D.rope_frequencies(8, scaling="base", factor=4)      # the fastest as it was, the slowest / 4
+    assert g[0] == 1.0 and abs(float(g[3] / f[3]) - 0.25) < 1e-12
+    g, m = D.rope_frequencies(128, scaling="parts", factor=8, trained=8192)
+    f, _ = D.rope_frequencies(128)
+    turns = 8192 * f / (2 * math.pi)
+    assert torch.equal(g[turns >= 32], f[turns >= 32]) and torch.allclose(g[turns <= 1], f[turns <= 1] / 8, rtol=1e-14)
+    assert ((g <= f) & (g >= f / 8 * (1 - 1e-12))).all() and abs(m - (0.1 * math.log(8) + 1)) < 1e-15
+    for bad in (0, 3, -2):
+        _refused("MOE_ERR_SHAPE", "rotary", D.rope_frequencies, bad)
+    _refused("MOE_ERR_INVALID_ARG", "scaling", D.rope_frequencies, 8, scaling="x")
+
+
+def test_masks_and_depths():
+    par = [-1, 0, 0, 1, 3]
+    assert D.tree_depths(par) == [0, 1, 1, 2, 3]
+    assert D.tree_masks(par) == [1, 3, 5, 11, 27]
+    chain = D.tree_masks(list(range(-1, 63)))
+    assert chain[62] == (1 << 63) - 1 and chain[63] == -1
+    _refused("MOE_ERR_ROWS", "65 rows", D.tree_masks, list(range(-1, 64)))
+    _refused("MOE_ERR_INVALID_ARG", "parent", D.tree_masks, [-1, 1])
