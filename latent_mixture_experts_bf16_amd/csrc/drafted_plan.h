@@ -38,6 +38,18 @@ struct RopeParams {
     int32_t rows, q_heads;
 };
 
+// Workgroups of the attention kernel that a compute unit holds at once: by LDS (two buffers of 64
+// tokens take 512 dim bytes of 160 KB) and by the registers of a wave's queries and sums.
+constexpr int attend_blocks(int dim, int queries) {
+    return dim <= 64 ? (queries == 16 ? 4 : 3) : dim <= 96 ? 3 : dim <= 128 ? 2 : 1;
+}
+
+// The first part of an item of attention work that was cut between workgroups: written by the range
+// that holds it, read by the launch that joins the parts.
+struct AttendPart {
+    int32_t count, first, mt, head, queries, pad[3];   // count 0: this range starts no cut item
+};
+
 struct AttendParams {
     CacheParams c;
     const uint16_t *q;
@@ -47,6 +59,10 @@ struct AttendParams {
     const uint64_t *mask;
     float scale_log2;           // scale * log2(e): scores are exponents of 2
     int32_t rows, q_heads, group;
+    int32_t tile_queries;
+    AttendPart *parts;          // [ranges]
+    float *part_stat;           // [2 ranges][2][tile_queries]: maximum, sum
+    float *part_sum;            // [2 ranges][tile_queries][dim]
 };
 
 constexpr int MAX_VOCAB = 1 << 20;

@@ -10,7 +10,8 @@
 
 namespace moe {
 template <bool F16, bool HALF, int W> __global__ void moe_rope_kernel(RopeParams p);
-template <bool F16> __global__ void moe_attend_kernel(AttendParams p);
+template <bool F16, int D, int NQ, int QW> __global__ void moe_attend_kernel(AttendParams p);
+template <bool F16, int D> __global__ void moe_attend_join_kernel(AttendParams p);
 template <typename L> __global__ void moe_verify_kernel(VerifyParams p);
 struct LogitF32;
 struct LogitBf16;
@@ -177,6 +178,14 @@ static int check_words(const char *name, const void *p, int align = 4) {
     return MOE_OK;
 }
 
+static int check_workspace(const void *p, size_t bytes, int64_t need) {
+    if (need && !p) return api_fail(MOE_ERR_INVALID_ARG, "workspace: NULL");
+    if ((uintptr_t)p & 15) return api_fail(MOE_ERR_LAYOUT, "workspace: not 16-byte aligned");
+    if (bytes < (size_t)need)
+        return api_fail(MOE_ERR_SHAPE, "workspace: %zu bytes, %lld needed", bytes, (long long)need);
+    return MOE_OK;
+}
+
 static bool overlap(const void *a, int64_t abytes, const void *b, int64_t bbytes) {
     const char *x = (const char *)a, *y = (const char *)b;
     return x < y + bbytes && y < x + abytes;
@@ -266,12 +275,59 @@ extern "C" int moe_rope_append(const moe_paged_cache *c, const moe_rope *r, int3
 
 // ------------------------------------------------------------------ tree attention
 
+typedef void (*AttendKernel)(AttendParams);
+
+template <bool F16, int D> static AttendKernel attend_kernel(int queries) {
+    return queries == 16   ? moe_attend_kernel<F16, D, 1, 1>
+           : queries == 32 ? moe_attend_kernel<F16, D, 2, 1>
+           : queries == 64 ? moe_attend_kernel<F16, D, 2, 2>
+                           : moe_attend_kernel<F16, D, 2, 4>;
+}
+template <bool F16> static void attend_kernels(int dim, int queries, AttendKernel *main, AttendKernel *join) {
+    switch (dim) {
+#define ATTEND_DIM(D)                            \
+    case D:                                      \
+        *main = attend_kernel<F16, D>(queries);  \
+        *join = moe_attend_join_kernel<F16, D>;  \
+        break
+        ATTEND_DIM(32);
+        ATTEND_DIM(64);
+        ATTEND_DIM(80);
+        ATTEND_DIM(96);
+        ATTEND_DIM(112);
+        ATTEND_DIM(128);
+        ATTEND_DIM(192);
+        default: ATTEND_DIM(256);
+#undef ATTEND_DIM
+    }
+}
+
+// How the work is cut (the lengths are known on the device only): queries of a tile, ranges of
+// work, blocks along the queries of the launch that joins parts; and the workspace's layout.
+struct AttendShape {
+    int queries, ranges, join;
+    int64_t stat, sum, bytes;
+};
+static AttendShape attend_shape(const CacheParams &c, int32_t rows, int32_t q_heads) {
+    AttendShape s;
+    // The queries that share a key head, on average over the sequences; a third more, since trees differ
+    // in size and a second query tile reads the cache again.
+    const int64_t mean = ((int64_t)rows * (q_heads / c.heads) + c.seqs - 1) / c.seqs, likely = mean + mean / 3;
+    s.queries = likely <= 16 ? 16 : likely <= 32 ? 32 : likely <= 64 ? 64 : 128;
+    s.ranges = 256 * attend_blocks(c.dim, s.queries);     // as many workgroups as 256 compute units hold at once
+    s.join = mean <= 4 ? 4 : mean <= 8 ? 8 : 16;
+    s.stat = (int64_t)s.ranges * sizeof(AttendPart);
+    s.sum = s.stat + (int64_t)s.ranges * 2 * 2 * s.queries * 4;
+    s.bytes = s.sum + (int64_t)s.ranges * 2 * s.queries * c.dim * 4;
+    return s;
+}
+
 extern "C" int64_t moe_tree_attend_workspace(const moe_paged_cache *c, int32_t rows, int32_t q_heads) {
     api_clear();
     CacheParams p;
     int rc;
     if ((rc = check_cache(c, p)) || (rc = check_rows(rows, q_heads, p))) return -rc;
-    return 0;
+    return attend_shape(p, rows, q_heads).bytes;
 }
 
 extern "C" int moe_tree_attend(const moe_paged_cache *c, int32_t rows, const void *q, int64_t q_stride,
@@ -291,7 +347,8 @@ extern "C" int moe_tree_attend(const moe_paged_cache *c, int32_t rows, const voi
     if (!std::isfinite(scale)) return api_fail(MOE_ERR_INVALID_ARG, "scale is not finite");
     if (rows_overlap(out, out_stride, w, q, q_stride, w, rows))
         return api_fail(MOE_ERR_ALIAS, "out overlaps q");
-    if ((rc = device_cus(&cus))) return rc;
+    const AttendShape shape = attend_shape(p.c, rows, q_heads);
+    if ((rc = check_workspace(workspace, workspace_bytes, shape.bytes)) || (rc = device_cus(&cus))) return rc;
     p.q = (const uint16_t *)q;
     p.out = (uint16_t *)out;
     p.q_stride = q_stride;
@@ -302,10 +359,17 @@ extern "C" int moe_tree_attend(const moe_paged_cache *c, int32_t rows, const voi
     p.rows = rows;
     p.q_heads = q_heads;
     p.group = q_heads / p.c.heads;
-    (void)workspace;
-    (void)workspace_bytes;
-    return launch("tree_attend", c->k.dtype == MOE_DT_F16 ? moe_attend_kernel<true> : moe_attend_kernel<false>,
-                  dim3((unsigned)rows, (unsigned)q_heads), dim3(256), p, hip_stream);
+    p.tile_queries = shape.queries;
+    p.parts = (AttendPart *)workspace;
+    p.part_stat = (float *)((char *)workspace + shape.stat);
+    p.part_sum = (float *)((char *)workspace + shape.sum);
+    AttendKernel main, join;
+    if (c->k.dtype == MOE_DT_F16)
+        attend_kernels<true>(p.c.dim, shape.queries, &main, &join);
+    else
+        attend_kernels<false>(p.c.dim, shape.queries, &main, &join);
+    if ((rc = launch("tree_attend", main, dim3((unsigned)shape.ranges), dim3(256), p, hip_stream))) return rc;
+    return launch("tree_attend join", join, dim3((unsigned)shape.ranges, (unsigned)shape.join), dim3(256), p, hip_stream);
 }
 
 // ------------------------------------------------------------------ draft verification
