@@ -23,6 +23,7 @@ typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
@@ -52,15 +53,25 @@ template <bool F16> __device__ __forceinline__ uint32_t pack2(float a, float b) 
 }
 
 // Whether one of two packed elements is infinite or NaN.
-template <bool F16> __device__ __forceinline__ bool odd2(uint32_t v) {
+template <bool F16> __device__ __forceinline__ int odd2(uint32_t v) {
     constexpr uint32_t E = F16 ? 0x7C00u : 0x7F80u;
-    return (v & E) == E || (v >> 16 & E) == E;
+    return (int)((v & E) == E) | (int)((v >> 16 & E) == E);
 }
 
 // The 4 x 16 elements that 16 lanes' addresses name (four lanes a row of 16), transposed: lane i
 // gets column i, one element of each row.
 __device__ __forceinline__ s16x4 read_columns(const uint16_t *lds) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)lds);
+}
+
+// The largest value of the four lanes that share a column.
+__device__ __forceinline__ float across_quads_max(float v) {
+    const uint32_t x = __float_as_uint(v);
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    const uint32_t y = __float_as_uint(v);
+    const auto q = __builtin_amdgcn_permlane16_swap(y, y, false, false);
+    return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
 }
 
 constexpr int low_bit(int v) { return v & -v; }
@@ -213,7 +224,7 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
 
         s16x8 qf[NQ][KS];
         uint64_t mask[NQ];
-        int qi[NQ];
+        int late[NQ];                     // the last row past the 64th that is seen
         f32x4 o[NQ][DB];
         float m[NQ], l[NQ];
 #pragma unroll
@@ -222,45 +233,44 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
             const bool ok = q < queries;
             const int i = ok ? z / p.group : 0, g = ok ? z - i * p.group : 0;
             const uint16_t *src = p.q + (int64_t)(first + i) * p.q_stride + (int64_t)(h * p.group + g) * D;
-            qi[u] = i;
-            mask[u] = p.mask ? p.mask[first + i] : 0;
+            // without masks: the rows up to its own
+            mask[u] = p.mask ? p.mask[first + i] : i < 63 ? (2ull << i) - 1 : ~0ull;
+            late[u] = p.mask ? -1 : i;
 #pragma unroll
             for (int k = 0; k < KS; ++k)
-                qf[u][k] = ok && k * 32 + quad * 8 < D ? *(const s16x8 *)(src + k * 32 + quad * 8) : s16x8{0, 0, 0, 0, 0, 0, 0, 0};
+                qf[u][k] = ok && k * 32 + quad * 8 < D ? *(const s16x8 *)(src + k * 32 + quad * 8) ^ p.q_sign
+                                                       : s16x8{0, 0, 0, 0, 0, 0, 0, 0};
             m[u] = -__builtin_inff();
             l[u] = 0.0f;
 #pragma unroll
             for (int d = 0; d < DB; ++d) o[u][d] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
-        // whether the query of this lane's column sees token t, which is not before len
+        // whether the query of this lane's column sees token t (without branches)
         auto sees = [&](int u, int t) {
             const int j = t - len;
-            return j < 0 || (p.mask ? j < 64 && (mask[u] >> j & 1) : j <= qi[u]);
+            return (int)(j < 0) | ((int)(j < 64) & (int)(mask[u] >> (j & 63)) & 1) | ((int)(j >= 64) & (int)(j <= late[u]));
         };
 
         const int32_t *table = p.c.table + b * p.c.table_stride;
-        uint4 kr[LOADS], vr[LOADS];
+        u32x4 kr[LOADS], vr[LOADS];
         // the page of this wave's group of a tile; looked up a tile before it is needed
         auto page_of = [&](int tile) {
             const int t = tile * 64 + wave * 16;
             return t < end ? table[t / p.c.page] : -1;
         };
+        // A group without a page reads the first one's slots instead: its scores are masked and its values zeroed.
         auto load = [&](int tile, int page) {
             const int t = tile * 64 + wave * 16;
             const bool ok = t < end && page >= 0 && page < p.c.pages;
-            if (ok) {
-                const int slot = t % p.c.page;
-                const char *kb = (const char *)(p.c.k.p + page * p.c.k.page + slot * p.c.k.slot + h * p.c.k.head);
-                const char *vb = (const char *)(p.c.v.p + page * p.c.v.page + slot * p.c.v.slot + h * p.c.v.head);
+            if (!ok && t < end && lane == 0) raise_flag(p.c.flags, MOE_FLAG_PAGE);
+            const int slot = t % p.c.page;
+            const int64_t pg = ok ? page : 0;
+            const char *kb = (const char *)(p.c.k.p + pg * p.c.k.page + slot * p.c.k.slot + h * p.c.k.head);
+            const char *vb = (const char *)(p.c.v.p + pg * p.c.v.page + slot * p.c.v.slot + h * p.c.v.head);
 #pragma unroll
-                for (int k = 0; k < LOADS; ++k) kr[k] = *(const uint4 *)(kb + ko[k]);
+            for (int k = 0; k < LOADS; ++k) kr[k] = *(const u32x4 *)(kb + ko[k]);
 #pragma unroll
-                for (int k = 0; k < LOADS; ++k) vr[k] = *(const uint4 *)(vb + vo[k]);
-            } else {
-                if (t < end && lane == 0) raise_flag(p.c.flags, MOE_FLAG_PAGE);
-#pragma unroll
-                for (int k = 0; k < LOADS; ++k) kr[k] = vr[k] = make_uint4(0, 0, 0, 0);
-            }
+            for (int k = 0; k < LOADS; ++k) vr[k] = *(const u32x4 *)(vb + vo[k]);
             return ok || t >= end;
         };
 
@@ -274,23 +284,23 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
             const int buf = tile & 1, t0 = tile * 64;
             uint16_t *const kl = lds[buf][0], *const vl = lds[buf][1];
             int told = good ? 0 : 1;
-            if (t0 + wave * 16 + 16 > len) {
+            if (t0 + wave * 16 + 16 > len || !good) {
                 // the step's own tokens: slots behind the last hold anything, and are zeroed; a value that is not finite
                 // must not reach the rows that do not see it
-                bool odd = false;
+                int odd = 0;
 #pragma unroll
                 for (int k = 0; k < LOADS; ++k) {
                     const int t = t0 + wave * 16 + pt[k];
-                    if (t >= end) vr[k] = make_uint4(0, 0, 0, 0);
-                    if (t >= len) odd |= odd2<F16>(vr[k].x) || odd2<F16>(vr[k].y) || odd2<F16>(vr[k].z) || odd2<F16>(vr[k].w);
+                    if (t >= end || !good) vr[k] = u32x4{0, 0, 0, 0};
+                    odd |= (int)(t >= len) & (odd2<F16>(vr[k].x) | odd2<F16>(vr[k].y) | odd2<F16>(vr[k].z) | odd2<F16>(vr[k].w));
                 }
                 if (__any(odd)) told |= 2;
             }
 #pragma unroll
             for (int k = 0; k < LOADS; ++k)
                 if (!RAGGED || k * 64 + lane < PIECES) {
-                    *(uint4 *)(kl + kp[k]) = kr[k];
-                    *(uint4 *)(vl + vp[k]) = vr[k];
+                    *(u32x4 *)(kl + kp[k]) = kr[k];
+                    *(u32x4 *)(vl + vp[k]) = vr[k];
                 }
             if (lane == 0) note[buf][wave] = told;
             if (tile + 1 < t_last) {
@@ -299,7 +309,7 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
             }
             __syncthreads();
             const int4 notes = *(const int4 *)note[buf];
-            const int all = uniform(notes.x | notes.y | notes.z | notes.w);
+            const int all = uniform(notes.x | notes.y << 4 | notes.z << 8 | notes.w << 12);   // four bits a group
             const bool special = t0 + 64 > len || all;
 
             f32x4 s[NS][NQ];
@@ -317,26 +327,28 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
                     for (int u = 0; u < NQ; ++u) s[a][u] = mfma32<F16>(f, qf[u][k], s[a][u]);
                 }
             }
+            if (special) {
+#pragma unroll
+                for (int a = 0; a < NS; ++a) {
+                    const int g = wt * NS + a, good_page = ~(all >> 4 * g);
+#pragma unroll
+                    for (int u = 0; u < NQ; ++u)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int t = t0 + g * 16 + quad * 4 + r;
+                            s[a][u][r] = sees(u, t) & (int)(t < end) & good_page & 1 ? s[a][u][r] : -__builtin_inff();
+                        }
+                }
+            }
             uint32_t pr[NS][NQ][2];
 #pragma unroll
             for (int u = 0; u < NQ; ++u) {
-                float top = m[u];
+                float top = -__builtin_inff();
 #pragma unroll
                 for (int a = 0; a < NS; ++a)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float v = s[a][u][r] * p.scale_log2;
-                        if (special) {
-                            const int g = wt * NS + a;
-                            const int bad = g == 0 ? notes.x : g == 1 ? notes.y : g == 2 ? notes.z : notes.w;
-                            if ((bad & 1) || !sees(u, t0 + g * 16 + quad * 4 + r) || t0 + g * 16 + quad * 4 + r >= end)
-                                v = -__builtin_inff();
-                        }
-                        s[a][u][r] = v;
-                        top = fmaxf(top, v);
-                    }
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
+                    for (int r = 0; r < 4; ++r) top = fmaxf(top, s[a][u][r]);
+                top = fmaxf(m[u], across_quads_max(top) * p.scale_log2);
                 const float from = top == -__builtin_inff() ? 0.0f : top;
                 if (__any(top > m[u])) {
                     const float keep = __builtin_amdgcn_exp2f(m[u] - from);
@@ -349,30 +361,34 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
                 for (int a = 0; a < NS; ++a) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        s[a][u][r] = __builtin_amdgcn_exp2f(s[a][u][r] - from);
+                        s[a][u][r] = __builtin_amdgcn_exp2f(fmaf(s[a][u][r], p.scale_log2, -from));
                         l[u] += s[a][u][r];
                     }
                     pr[a][u][0] = pack2<F16>(s[a][u][0], s[a][u][1]);
                     pr[a][u][1] = pack2<F16>(s[a][u][2], s[a][u][3]);
                 }
             }
-            if (all & 2) {
+            if (all & 0x2222) {
                 // values that are not finite: added for the rows that see them, then taken out of the tile, so that
                 // no probability of 0 meets them
                 for (int t = 0; t < NS * 16; ++t) {
                     const int tt = wt * NS * 16 + t;
                     const uint16_t *row = vl + (tt >> 4) * GE;
                     if (t0 + tt < len) continue;
+                    int see[NQ];
 #pragma unroll
-                    for (int d = 0; d < DB; ++d)
+                    for (int u = 0; u < NQ; ++u) see[u] = sees(u, t0 + tt);
+#pragma unroll
+                    for (int d = 0; d < DB; ++d) {
+                        const uint2 e = *(const uint2 *)(row + v_unit<D>(tt & 15, d) + quad * 4);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const uint32_t e = row[v_unit<D>(tt & 15, d) + quad * 4 + r];
-                            if (odd2<F16>(e))
+                            const uint32_t v = (r < 2 ? e.x : e.y) >> (r & 1) * 16 & 0xFFFFu;
+                            const float add = odd2<F16>(v) ? to_f32<F16>(v) : 0.0f;
 #pragma unroll
-                                for (int u = 0; u < NQ; ++u)
-                                    if (sees(u, t0 + tt)) o[u][d][r] += to_f32<F16>(e);
+                            for (int u = 0; u < NQ; ++u) o[u][d][r] += see[u] ? add : 0.0f;
                         }
+                    }
                 }
                 __syncthreads();
                 for (int e = tid; e < 4 * GE; e += 256)
@@ -467,53 +483,58 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
     }
 }
 
-// Joins the parts of cut items: block (w, y) those of the item whose first part range w holds, queries
-// y, y + gridDim.y, ... The threads lie along the head (D / 4 of them) and along the parts.
+// Joins the parts of cut items: block (w, y) those of the item whose first part range w holds. A wave
+// joins one query at a time: the parts' maxima and sums lie along its lanes, 64 parts a step, and then
+// its lanes lie along the head (D / 4 of them) and along the parts.
 template <bool F16, int D>
 __global__ void __launch_bounds__(256) moe_attend_join_kernel(AttendParams p) {
-    constexpr int U = D / 4, PL = 256 / U;     // threads along the head, along the parts
-    __shared__ float sm[PL], ss[PL];
-    __shared__ f32x4 so[PL][U];
-    const int w = (int)blockIdx.x, tid = (int)threadIdx.x, u = tid % U, k = tid / U, MQ = p.tile_queries;
+    constexpr int U = D / 4, PL = 64 / U;
+    const int w = (int)blockIdx.x, lane = lane_id(), wave = uniform((int)threadIdx.x >> 6), MQ = p.tile_queries;
     const AttendPart part = p.parts[w];
-    for (int q = (int)blockIdx.y; q < part.queries && part.count > 0; q += (int)gridDim.y) {
-        // part a: slot 1 of range w, then slot 0 of the ranges after it
-        float m = -__builtin_inff(), s = 0.0f;
+    if (part.count <= 0) return;
+    const int k = lane / U, u = lane % U;
+    for (int q = (int)blockIdx.y * 4 + wave; q < part.queries; q += (int)gridDim.y * 4) {
+        float top = -__builtin_inff(), sum = 0.0f;
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
-        if (k < PL) {
-            for (int a = k; a < part.count; a += PL) {
-                const int64_t slot = a ? 2 * (w + a) : 2 * w + 1;
-                m = fmaxf(m, p.part_stat[slot * 2 * MQ + q]);
+        for (int a0 = 0; a0 < part.count; a0 += 64) {
+            // part a: slot 1 of range w, then slot 0 of the ranges after it
+            const int a = a0 + lane, here = min(64, part.count - a0);
+            float m = -__builtin_inff(), s = 0.0f;
+            if (a < part.count) {
+                const int64_t slot = a ? 2 * (int64_t)(w + a) : 2 * (int64_t)w + 1;
+                m = p.part_stat[slot * 2 * MQ + q];
+                s = p.part_stat[slot * 2 * MQ + MQ + q];
             }
-            const float from = m == -__builtin_inff() ? 0.0f : m;
-#pragma unroll 4
-            for (int a = k; a < part.count; a += PL) {
-                const int64_t slot = a ? 2 * (w + a) : 2 * w + 1;
-                const float f = __builtin_amdgcn_exp2f(p.part_stat[slot * 2 * MQ + q] - from);
-                s += f * p.part_stat[slot * 2 * MQ + MQ + q];
-                o += f * *(const f32x4 *)(p.part_sum + (slot * MQ + q) * D + u * 4);
+            float best = fmaxf(top, m);
+            for (int d = 32; d; d >>= 1) best = fmaxf(best, __shfl_xor(best, d));
+            const float from = best == -__builtin_inff() ? 0.0f : best;
+            const float old = __builtin_amdgcn_exp2f(top - from), f = __builtin_amdgcn_exp2f(m - from);
+            sum = sum * old + f * s;
+            o *= old;
+            top = best;
+            const int steps = (here + PL - 1) / PL;
+#pragma unroll 8
+            for (int i = 0; i < steps; ++i) {
+                const int at = i * PL + k;
+                const float g = __shfl(f, at & 63);
+                if (k < PL && at < here) {
+                    const int64_t slot = a0 + at ? 2 * (int64_t)(w + a0 + at) : 2 * (int64_t)w + 1;
+                    o += g * *(const f32x4 *)(p.part_sum + (slot * MQ + q) * D + u * 4);
+                }
             }
-            so[k][u] = o;
-            if (u == 0) { sm[k] = m; ss[k] = s; }
         }
-        __syncthreads();
+        for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+        f32x4 all = o;
+        for (int j = 1; j < PL; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) all[e] += __shfl(o[e], (lane + j * U) & 63);
         if (k == 0) {
-            float top = sm[0], sum = 0.0f;
-            for (int a = 1; a < PL; ++a) top = fmaxf(top, sm[a]);
-            const float from = top == -__builtin_inff() ? 0.0f : top;
-            f32x4 all = {0.f, 0.f, 0.f, 0.f};
-            for (int a = 0; a < PL; ++a) {
-                const float f = __builtin_amdgcn_exp2f(sm[a] - from);
-                sum += f * ss[a];
-                all += f * so[a][u];
-            }
             const int z = part.mt * MQ + q, i = z / p.group, g = z - i * p.group;
             const float inv = 1.0f / sum;
             const f32x4 r = sum == 0.0f ? f32x4{0.f, 0.f, 0.f, 0.f} : all * inv;
             *(uint2 *)(p.out + (int64_t)(part.first + i) * p.out_stride + (int64_t)(part.head * p.group + g) * D + u * 4) =
                 make_uint2(pack2<F16>(r[0], r[1]), pack2<F16>(r[2], r[3]));
         }
-        __syncthreads();
     }
 }
 

@@ -57,7 +57,8 @@ struct AttendParams {
     int64_t q_stride, out_stride;
     const int32_t *row_start;
     const uint64_t *mask;
-    float scale_log2;           // scale * log2(e): scores are exponents of 2
+    float scale_log2;           // |scale| * log2(e), above 0: scores are exponents of 2
+    int16_t q_sign;             // xor on the queries: the sign bit where the scale is negative
     int32_t rows, q_heads, group;
     int32_t tile_queries;
     AttendPart *parts;          // [ranges]

@@ -310,12 +310,12 @@ struct AttendShape {
 };
 static AttendShape attend_shape(const CacheParams &c, int32_t rows, int32_t q_heads) {
     AttendShape s;
-    // The queries that share a key head, on average over the sequences; a third more, since trees differ
-    // in size and a second query tile reads the cache again.
-    const int64_t mean = ((int64_t)rows * (q_heads / c.heads) + c.seqs - 1) / c.seqs, likely = mean + mean / 3;
-    s.queries = likely <= 16 ? 16 : likely <= 32 ? 32 : likely <= 64 ? 64 : 128;
+    // The least tile that holds the queries that share a key head, on average over the sequences (their
+    // own numbers are on the device): a sequence with more of them reads its cache again.
+    const int64_t mean = ((int64_t)rows * (q_heads / c.heads) + c.seqs - 1) / c.seqs;
+    s.queries = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
     s.ranges = 256 * attend_blocks(c.dim, s.queries);     // as many workgroups as 256 compute units hold at once
-    s.join = mean <= 4 ? 4 : mean <= 8 ? 8 : 16;
+    s.join = mean <= 4 ? 1 : mean <= 16 ? 4 : 16;     // of four queries each
     s.stat = (int64_t)s.ranges * sizeof(AttendPart);
     s.sum = s.stat + (int64_t)s.ranges * 2 * 2 * s.queries * 4;
     s.bytes = s.sum + (int64_t)s.ranges * 2 * s.queries * c.dim * 4;
@@ -355,7 +355,10 @@ extern "C" int moe_tree_attend(const moe_paged_cache *c, int32_t rows, const voi
     p.out_stride = out_stride;
     p.row_start = row_start;
     p.mask = mask;
-    p.scale_log2 = scale * 1.44269504088896340736f;
+    // The kernel takes maxima of unscaled scores, so its factor is positive: a negative scale turns the queries'
+    // signs instead, and one of 0 (or nearly) becomes so small that all weights are 1.
+    p.scale_log2 = std::fmax(std::fabs(scale) * 1.44269504088896340736f, 1e-30f);
+    p.q_sign = scale < 0 ? (int16_t)0x8000 : 0;
     p.rows = rows;
     p.q_heads = q_heads;
     p.group = q_heads / p.c.heads;
