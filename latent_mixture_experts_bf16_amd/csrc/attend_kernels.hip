@@ -91,10 +91,14 @@ template <int D> __device__ __forceinline__ int v_unit(int t, int u) {
     return t * D + (u ^ ((t >> SH) & (P - 1))) * 16;
 }
 
-// Tiles of sequence b: rows, tokens, and how they are cut.
+// Work of sequence b: rows, tokens, and how they are cut. An item counts as its tiles and ITEM_COST more,
+// for its start and end, in which no tile is in flight: so a range of many short items takes no longer
+// than one of a long one (an empty sequence beside seven of 8200 tokens: 108 -> 58 us
+// at 16 rows).
+constexpr int ITEM_COST = 3;
 struct SeqWork {
     int first, n, len, end, mts, tts;
-    int64_t tiles;
+    int64_t units;
 };
 template <int MQ> __device__ __forceinline__ SeqWork seq_work(const AttendParams &p, int b, bool tell) {
     SeqWork w;
@@ -107,7 +111,7 @@ template <int MQ> __device__ __forceinline__ SeqWork seq_work(const AttendParams
     w.end = past ? p.c.cap : w.len + w.n;
     w.mts = (int)(((int64_t)w.n * p.group + MQ - 1) / MQ);
     w.tts = (int)(((int64_t)w.end + 63) >> 6);
-    w.tiles = (int64_t)w.mts * w.tts * p.c.heads;
+    w.units = (int64_t)w.mts * (w.tts + ITEM_COST) * p.c.heads;
     if (tell) {
         const uint32_t f = (rows_bad ? MOE_FLAG_ROWS : 0) | (len_bad ? MOE_FLAG_LEN : 0) | (past ? MOE_FLAG_PAGE : 0);
         if (f) raise_flag(p.c.flags, f);
@@ -121,8 +125,8 @@ struct PlanLds {
     int b;
 };
 
-// All tiles, and the range of them that this workgroup has: [x, xe), starting in sequence b whose
-// tiles start at base. false: none. Each thread sums a run of sequences.
+// All units of work, and the range of them that this workgroup has: [x, xe), starting in sequence b
+// whose units start at base. false: none. Each thread sums a run of sequences.
 template <int MQ>
 __device__ __forceinline__ bool find_range(const AttendParams &p, PlanLds &s, int *w, int64_t *total, int64_t *groups,
                                            int64_t *x, int64_t *xe, int *b, int64_t *base) {
@@ -131,7 +135,7 @@ __device__ __forceinline__ bool find_range(const AttendParams &p, PlanLds &s, in
     int64_t sum = 0;
     for (int k = 0; k < per; ++k) {
         const int q = tid * per + k;
-        if (q < p.c.seqs) sum += seq_work<MQ>(p, q, tell).tiles;
+        if (q < p.c.seqs) sum += seq_work<MQ>(p, q, tell).units;
     }
     if (tell && tid == 0 && (p.row_start[0] != 0 || p.row_start[p.c.seqs] != p.rows))
         raise_flag(p.c.flags, MOE_FLAG_ROWS);
@@ -159,7 +163,7 @@ __device__ __forceinline__ bool find_range(const AttendParams &p, PlanLds &s, in
     *xe = (at + 1) * N / G;
     if (sum && before <= *x && *x < before + sum) {
         int q = tid * per;
-        for (int64_t t; *x >= before + (t = seq_work<MQ>(p, q, false).tiles); ++q) before += t;
+        for (int64_t t; *x >= before + (t = seq_work<MQ>(p, q, false).units); ++q) before += t;
         s.b = q;
         s.base = before;
     }
@@ -204,16 +208,20 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
 
     while (x < xe) {
         SeqWork sq = seq_work<MQ>(p, b, false);
-        if (x >= base + sq.tiles) {
-            base += sq.tiles;
+        if (x >= base + sq.units) {
+            base += sq.units;
             ++b;
             continue;
         }
         const int first = uniform(sq.first), n = uniform(sq.n), len = uniform(sq.len), end = uniform(sq.end);
-        const int64_t rel = x - base, item = rel / sq.tts;
-        const int t_from = uniform((int)(rel - item * sq.tts)), tts = uniform(sq.tts), mts = uniform(sq.mts);
+        const int tts = uniform(sq.tts), mts = uniform(sq.mts), all_units = tts + ITEM_COST;
+        const int64_t rel = x - base, item = rel / all_units;
+        const int u_from = uniform((int)(rel - item * all_units));
+        const int u_to = uniform((int)min((int64_t)all_units, u_from + (xe - x)));
+        const int t_from = max(0, u_from - ITEM_COST), t_to = u_to - ITEM_COST;
         const int mt = uniform((int)(item % mts)), h = uniform((int)(item / mts));
-        const int t_to = uniform((int)min((int64_t)tts, t_from + (xe - x)));
+        x += u_to - u_from;
+        if (t_to <= t_from) continue;
         const int queries = min((int64_t)MQ, (int64_t)n * p.group - (int64_t)mt * MQ);
         // rows without a mask see no token after their own: tiles past the last row's are not read
         int t_last = t_to;
@@ -471,70 +479,147 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
         }
         if (!whole && t_from == 0 && tid == 0) {
             // the first part of a cut item: the ranges that hold it are this one and the next ones
-            const int64_t last = x + tts;
+            const int64_t last = x - u_to + all_units;
             part.first = first;
             part.mt = mt;
             part.head = h;
             part.queries = queries;
             part.count = (int)((last * groups - 1) / total) - w + 1;
         }
-        x += t_to - t_from;
         __syncthreads();
     }
 }
 
-// Joins the parts of cut items: block (w, y) those of the item whose first part range w holds. A wave
-// joins one query at a time: the parts' maxima and sums lie along its lanes, 64 parts a step, and then
-// its lanes lie along the head (D / 4 of them) and along the parts.
+// What some parts of one query sum to.
+struct JoinSum {
+    float top, sum;   // sum: this lane's share
+    f32x4 o;
+};
+
+// One wave adds parts [lo, hi) of query q of the item that begins in range w (part a lies in slot 1 of
+// range w, then in slot 0 of the ranges after it). Maxima and sums lie along the lanes, 64 parts a
+// step; then the lanes lie along the head (D / 4 of them) and along the parts.
+template <int D> __device__ __forceinline__ JoinSum join_parts(const AttendParams &p, int w, int q, int lo, int hi) {
+    constexpr int U = D / 4, PL = 64 / U;
+    const int lane = lane_id(), k = lane / U, u = lane % U, MQ = p.tile_queries;
+    JoinSum j = {-__builtin_inff(), 0.0f, {0.f, 0.f, 0.f, 0.f}};
+    for (int a0 = lo; a0 < hi; a0 += 64) {
+        const int a = a0 + lane, here = min(64, hi - a0);
+        float m = -__builtin_inff(), s = 0.0f;
+        if (a < hi) {
+            const int64_t slot = 2 * (int64_t)(w + a) + (a == 0);
+            m = p.part_stat[slot * 2 * MQ + q];
+            s = p.part_stat[slot * 2 * MQ + MQ + q];
+        }
+        float best = fmaxf(j.top, m);
+        for (int d = 32; d; d >>= 1) best = fmaxf(best, __shfl_xor(best, d));
+        const float from = best == -__builtin_inff() ? 0.0f : best;
+        const float old = __builtin_amdgcn_exp2f(j.top - from), f = __builtin_amdgcn_exp2f(m - from);
+        j.sum = j.sum * old + f * s;
+        j.o *= old;
+        j.top = best;
+        for (int i0 = 0; i0 < here; i0 += 8 * PL) {
+            f32x4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {       // all on their way before the first is used
+                const int at = i0 + i * PL + k;
+                const int64_t slot = 2 * (int64_t)(w + a0 + at) + (a0 + at == 0);
+                v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (k < PL && at < here) v[i] = *(const f32x4 *)(p.part_sum + (slot * MQ + q) * D + u * 4);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int at = i0 + i * PL + k;
+                const float g = __shfl(f, at & 63);
+                j.o += (k < PL && at < here ? g : 0.0f) * v[i];
+            }
+        }
+    }
+    const f32x4 own = j.o;
+    for (int i = 1; i < PL; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) j.o[e] += __shfl(own[e], (lane + i * U) & 63);
+    for (int d = 32; d; d >>= 1) j.sum += __shfl_xor(j.sum, d);
+    return j;     // o in the lanes below U
+}
+
+// Joins the parts of cut items. Every workgroup lists the (item, query) pairs that the ranges' records
+// name; a pair is one wave's work, or, where there are no more of them than workgroups (few queries
+// over a long cache: many parts each), one workgroup's, its waves taking a quarter of the parts each.
 template <bool F16, int D>
 __global__ void __launch_bounds__(256) moe_attend_join_kernel(AttendParams p) {
-    constexpr int U = D / 4, PL = 64 / U;
-    const int w = (int)blockIdx.x, lane = lane_id(), wave = uniform((int)threadIdx.x >> 6), MQ = p.tile_queries;
-    const AttendPart part = p.parts[w];
-    if (part.count <= 0) return;
-    const int k = lane / U, u = lane % U;
-    for (int q = (int)blockIdx.y * 4 + wave; q < part.queries; q += (int)gridDim.y * 4) {
-        float top = -__builtin_inff(), sum = 0.0f;
-        f32x4 o = {0.f, 0.f, 0.f, 0.f};
-        for (int a0 = 0; a0 < part.count; a0 += 64) {
-            // part a: slot 1 of range w, then slot 0 of the ranges after it
-            const int a = a0 + lane, here = min(64, part.count - a0);
-            float m = -__builtin_inff(), s = 0.0f;
-            if (a < part.count) {
-                const int64_t slot = a ? 2 * (int64_t)(w + a) : 2 * (int64_t)w + 1;
-                m = p.part_stat[slot * 2 * MQ + q];
-                s = p.part_stat[slot * 2 * MQ + MQ + q];
-            }
-            float best = fmaxf(top, m);
-            for (int d = 32; d; d >>= 1) best = fmaxf(best, __shfl_xor(best, d));
-            const float from = best == -__builtin_inff() ? 0.0f : best;
-            const float old = __builtin_amdgcn_exp2f(top - from), f = __builtin_amdgcn_exp2f(m - from);
-            sum = sum * old + f * s;
-            o *= old;
-            top = best;
-            const int steps = (here + PL - 1) / PL;
-#pragma unroll 8
-            for (int i = 0; i < steps; ++i) {
-                const int at = i * PL + k;
-                const float g = __shfl(f, at & 63);
-                if (k < PL && at < here) {
-                    const int64_t slot = a0 + at ? 2 * (int64_t)(w + a0 + at) : 2 * (int64_t)w + 1;
-                    o += g * *(const f32x4 *)(p.part_sum + (slot * MQ + q) * D + u * 4);
-                }
-            }
-        }
-        for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
-        f32x4 all = o;
-        for (int j = 1; j < PL; ++j)
+    constexpr int U = D / 4;
+    __shared__ int start[ATTEND_MOST_RANGES + 1], wave_sum[4];
+    __shared__ float sm[4], ss[4];
+    __shared__ f32x4 so[4][U];
+    const int tid = (int)threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6), per = p.ranges >> 8;
+    int mine = 0, n[ATTEND_MOST_RANGES / 256];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) all[e] += __shfl(o[e], (lane + j * U) & 63);
-        if (k == 0) {
-            const int z = part.mt * MQ + q, i = z / p.group, g = z - i * p.group;
-            const float inv = 1.0f / sum;
-            const f32x4 r = sum == 0.0f ? f32x4{0.f, 0.f, 0.f, 0.f} : all * inv;
-            *(uint2 *)(p.out + (int64_t)(part.first + i) * p.out_stride + (int64_t)(part.head * p.group + g) * D + u * 4) =
+    for (int k = 0; k < ATTEND_MOST_RANGES / 256; ++k) {
+        n[k] = 0;
+        if (k < per) {
+            const AttendPart &part = p.parts[tid * per + k];
+            n[k] = part.count > 0 ? part.queries : 0;
+        }
+        mine += n[k];
+    }
+    int run = mine;
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(run, d);
+        if (lane >= d) run += v;
+    }
+    if (lane == 63) wave_sum[wave] = run;
+    __syncthreads();
+    int at = run - mine, total = 0;
+    for (int k = 0; k < 4; ++k) {
+        if (k < wave) at += wave_sum[k];
+        total += wave_sum[k];
+    }
+#pragma unroll
+    for (int k = 0; k < ATTEND_MOST_RANGES / 256; ++k)
+        if (k < per) {
+            start[tid * per + k] = at;
+            at += n[k];
+        }
+    if (tid == 0) start[p.ranges] = total;
+    __syncthreads();
+    const bool shared = total <= (int)gridDim.x;
+    const int step = shared ? (int)gridDim.x : (int)gridDim.x * 4;
+    for (int i = shared ? (int)blockIdx.x : (int)blockIdx.x * 4 + wave; i < total; i += step) {
+        int lo = 0, hi = p.ranges;       // the last range that starts at or before pair i: the one that holds it
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (start[mid] <= i) lo = mid; else hi = mid;
+        }
+        const int w = uniform(lo), q = uniform(i - start[lo]);
+        const AttendPart part = p.parts[w];
+        JoinSum j;
+        if (shared) {
+            const int each = (part.count + 3) >> 2;
+            j = join_parts<D>(p, w, q, min(part.count, wave * each), min(part.count, (wave + 1) * each));
+            if (lane < U) so[wave][lane] = j.o;
+            if (lane == 0) { sm[wave] = j.top; ss[wave] = j.sum; }
+            __syncthreads();
+            const float best = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3])), from = best == -__builtin_inff() ? 0.0f : best;
+            j.o = f32x4{0.f, 0.f, 0.f, 0.f};
+            j.sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float f = __builtin_amdgcn_exp2f(sm[k] - from);
+                j.sum += f * ss[k];
+                if (lane < U) j.o += f * so[k][lane];
+            }
+        } else {
+            j = join_parts<D>(p, w, q, 0, part.count);
+        }
+        if (lane < U && (!shared || wave == 0)) {
+            const int z = part.mt * p.tile_queries + q, row = z / p.group, g = z - row * p.group;
+            const float inv = 1.0f / j.sum;
+            const f32x4 r = j.sum == 0.0f ? f32x4{0.f, 0.f, 0.f, 0.f} : j.o * inv;
+            *(uint2 *)(p.out + (int64_t)(part.first + row) * p.out_stride + (int64_t)(part.head * p.group + g) * D + lane * 4) =
                 make_uint2(pack2<F16>(r[0], r[1]), pack2<F16>(r[2], r[3]));
         }
+        if (shared) __syncthreads();
     }
 }
 

@@ -21,20 +21,24 @@ template <bool F16> __device__ __forceinline__ float to_f32(uint32_t h) { return
 template <bool F16> __device__ __forceinline__ uint16_t from_f32(float v) { return F16 ? f2h(v) : f2bf(v); }
 
 // The sequence whose rows hold `row`, or -1: the last one that starts at or before it, if it also
-// ends after it. Every lane of the wave calls it with the same row; lanes read 64 starts at a time.
+// ends after it. Every lane of the wave calls it with the same row; the 64 lanes read starts that cut
+// what is left into 64, so 64 sequences take one step and 2^16 take three.
 __device__ __forceinline__ int seq_of_row(const int32_t *row_start, int seqs, int row, int *first) {
-    int before = 0;
-    for (int b0 = 0; b0 <= seqs; b0 += 64) {
-        const int b = b0 + lane_id();
-        const int s = b <= seqs ? row_start[b] : 0x7FFFFFFF;
-        const uint64_t le = __ballot(s <= row);
-        before += __popcll(le);
-        if (le != ~0ull) break;     // ascending: no later start is at or before the row
+    int lo = 0, n = seqs + 1;          // the starts lo .. lo + n - 1 are left
+    for (;;) {
+        const int step = (n + 63) >> 6, at = lane_id() * step;
+        const int s = at < n ? row_start[lo + at] : 0x7FFFFFFF;
+        const int before = __popcll(__ballot(s <= row));      // ascending: these are the first lanes
+        if (before == 0) return -1;
+        const int skip = (before - 1) * step;
+        lo += skip;
+        n = min(step, n - skip);
+        if (step == 1) break;
     }
-    const int b = uniform(before - 1);
-    if (b < 0 || b >= seqs) return -1;
+    const int b = uniform(lo);
+    if (b >= seqs) return -1;
     *first = uniform(row_start[b]);
-    return *first >= 0 && row < row_start[b + 1] ? b : -1;
+    return *first >= 0 && row >= *first && row < row_start[b + 1] ? b : -1;
 }
 
 // Rows of sequence b, bounded to the pass: [first, first + returned count).

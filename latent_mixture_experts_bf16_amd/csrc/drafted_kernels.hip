@@ -1,4 +1,4 @@
-// drafted_kernels.hip -- rotary append, draft verification and path keeping (gfx950).
+// drafted_kernels.hip -- rotary append and path keeping (gfx950).
 #include "drafted_items.h"
 
 namespace moe {
@@ -186,236 +186,5 @@ __global__ void __launch_bounds__(256) moe_keep_kernel(KeepParams p) {
     // every thread read the length before the barrier above, so the cache's own may be written
     if (tid == 0) p.new_len[b] = len + keep;
 }
-
-// ------------------------------------------------------------------ draft verification
-
-// Probabilities and their running sums decide which whole token comes out, so they are
-// held in 64 bits throughout: a running sum over 10^5 terms in 32 bits is off by more than the
-// probability of most tokens.
-struct LogitF32 {
-    static __device__ __forceinline__ float at(const void *z, int64_t i) { return ((const float *)z)[i]; }
-};
-struct LogitBf16 {
-    static __device__ __forceinline__ float at(const void *z, int64_t i) { return bf2f(((const uint16_t *)z)[i]); }
-};
-struct LogitF16 {
-    static __device__ __forceinline__ float at(const void *z, int64_t i) { return h2f(((const uint16_t *)z)[i]); }
-};
-
-// The weight of one token in a row: exp((z - top) / T) / Z - S q, not below 0; T <= 0: all on `best`.
-struct RowState {
-    float top;
-    int best;
-    double inv_t, inv_z, S;     // inv_t 0: greedy
-};
-
-template <typename L>
-__device__ __forceinline__ double target_weight(const RowState &r, const void *z, int64_t base, int i) {
-    if (r.inv_t == 0.0) return i == r.best ? 1.0 : 0.0;
-    const float x = L::at(z, base + i);
-    // equal first: the largest may be +infinity; NaN compares false and weighs nothing
-    return x == r.top ? r.inv_z : x < r.top ? exp(((double)x - (double)r.top) * r.inv_t) * r.inv_z : 0.0;
-}
-
-template <typename L>
-__device__ __forceinline__ double weight(const RowState &r, const void *z, int64_t base, const float *q, int64_t qbase,
-                                         int i) {
-    double w = target_weight<L>(r, z, base, i);
-    if (r.S > 0.0) {
-        w -= r.S * (double)q[qbase + i];
-        w = w > 0.0 ? w : 0.0;
-    }
-    return w;
-}
-
-__device__ __forceinline__ double wave_sum(double v) {
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-    return v;
-}
-__device__ __forceinline__ double wave_scan(double v) {     // inclusive
-    for (int d = 1; d < 64; d <<= 1) {
-        const double u = __shfl_up(v, d);
-        if (lane_id() >= d) v += u;
-    }
-    return v;
-}
-
-constexpr int VERIFY_THREADS = 1024, VERIFY_WAVES = VERIFY_THREADS / 64;
-
-struct VerifyLds {
-    double part[MAX_CHUNKS];
-    float wave_top[VERIFY_WAVES];
-    int wave_best[VERIFY_WAVES];
-    int pick;
-};
-
-// Sums of the row's weights by chunk into s.part; returns the whole sum, the same in every thread
-// (each wave adds the chunks in the same order).
-template <typename L>
-__device__ double sum_row(const RowState &r, const VerifyParams &p, int64_t base, int64_t qbase, VerifyLds &s) {
-    const int chunks = (p.vocab + VOCAB_CHUNK - 1) / VOCAB_CHUNK, wave = (int)threadIdx.x >> 6, lane = lane_id();
-    __syncthreads();
-    for (int c = wave; c < chunks; c += VERIFY_WAVES) {
-        double a = 0.0;
-        for (int i = c * VOCAB_CHUNK + lane; i < min(p.vocab, (c + 1) * VOCAB_CHUNK); i += 64)
-            a += weight<L>(r, p.logits, base, p.draft, qbase, i);
-        a = wave_sum(a);
-        if (lane == 0) s.part[c] = a;
-    }
-    __syncthreads();
-    double a = 0.0;
-    for (int c = lane; c < chunks; c += 64) a += s.part[c];
-    __syncthreads();
-    return wave_sum(a);
-}
-
-// The first index whose running sum passes u * (the whole sum), from the chunk sums in s.part.
-template <typename L>
-__device__ int pick_row(const RowState &r, const VerifyParams &p, int64_t base, int64_t qbase, double total, float u,
-                        VerifyLds &s) {
-    if (threadIdx.x < 64) {
-        const int chunks = (p.vocab + VOCAB_CHUNK - 1) / VOCAB_CHUNK, lane = lane_id();
-        const double target = (double)u * total;
-        // the chunk: the first whose running sum passes, or (a last rounding) the last with weight
-        double before = 0.0, at = 0.0;
-        int chunk = -1;
-        for (int c = 0; c < chunks; ++c) {
-            const double w = s.part[c];
-            if (w > 0.0) { chunk = c; at = before; }
-            before += w;
-            if (before > target) break;
-        }
-        int found = -1;
-        if (chunk >= 0) {
-            double run = at;
-            for (int i0 = chunk * VOCAB_CHUNK; i0 < min(p.vocab, (chunk + 1) * VOCAB_CHUNK); i0 += 64) {
-                const int i = i0 + lane;
-                const double w = i < p.vocab ? weight<L>(r, p.logits, base, p.draft, qbase, i) : 0.0;
-                const double cum = run + wave_scan(w);
-                const uint64_t some = __ballot(w > 0.0), past = __ballot(w > 0.0 && cum > target);
-                if (past) { found = i0 + __builtin_ctzll(past); break; }
-                if (some) found = i0 + 63 - __builtin_clzll(some);
-                run = __shfl(cum, 63);
-            }
-        }
-        if (lane == 0) s.pick = found < 0 ? 0 : found;
-    }
-    __syncthreads();
-    const int t = s.pick;
-    __syncthreads();
-    return t;
-}
-
-// One workgroup per sequence walks it.
-template <typename L>
-__global__ void __launch_bounds__(VERIFY_THREADS) moe_verify_kernel(VerifyParams p) {
-    __shared__ VerifyLds s;
-    const int b = (int)blockIdx.x, tid = (int)threadIdx.x, lane = lane_id(), wave = tid >> 6;
-    int first = 0;
-    const int n = seq_rows(p.row_start, b, p.rows, &first, p.flags);
-    if (n == 0) {
-        if (tid == 0) p.n_keep[b] = 0;
-        return;
-    }
-    const float T = p.temperature ? p.temperature[b] : 1.0f;
-    int cur = 0, kept = 1;
-    for (;;) {
-        const int row = first + cur;
-        const int64_t base = row * p.logit_stride, qbase = row * p.draft_stride;
-        // the largest logit, the lowest index among equals
-        float top = -__builtin_inff();
-        int best = p.vocab;
-        for (int i = tid; i < p.vocab; i += VERIFY_THREADS) {
-            const float x = L::at(p.logits, base + i);
-            if (x > top) { top = x; best = i; }
-        }
-        for (int d = 32; d; d >>= 1) {
-            const float t2 = __shfl_xor(top, d);
-            const int b2 = __shfl_xor(best, d);
-            if (t2 > top || (t2 == top && b2 < best)) { top = t2; best = b2; }
-        }
-        __syncthreads();
-        if (lane == 0) { s.wave_top[wave] = top; s.wave_best[wave] = best; }
-        __syncthreads();
-        for (int w = 0; w < VERIFY_WAVES; ++w) {
-            const float t2 = s.wave_top[w];
-            const int b2 = s.wave_best[w];
-            if (t2 > top || (t2 == top && b2 < best)) { top = t2; best = b2; }
-        }
-        RowState r;
-        r.top = top;
-        r.best = best;
-        r.S = 0.0;
-        r.inv_z = 1.0;
-        r.inv_t = T > 0.0f ? 1.0 / (double)T : 0.0;
-        if (best >= p.vocab) {       // nothing above -infinity: token 0, for want of a distribution
-            if (tid == 0) raise_flag(p.flags, MOE_FLAG_LOGITS);
-            r.best = 0;
-            r.inv_t = 0.0;
-        }
-        const double z = sum_row<L>(r, p, base, qbase, s);
-        r.inv_z = 1.0 / z;
-        double total = z * r.inv_z;
-        int token = -1, next = -1;
-        if (!p.draft) {
-            for (int c = tid; c < (p.vocab + VOCAB_CHUNK - 1) / VOCAB_CHUNK; c += VERIFY_THREADS) s.part[c] *= r.inv_z;
-            __syncthreads();
-            token = pick_row<L>(r, p, base, qbase, total, p.u_pick[row], s);
-            for (int c = cur + 1; c < n; ++c) {
-                if ((p.parent ? p.parent[first + c] : c - 1) != cur) continue;
-                const int x = p.tokens[first + c];
-                if (x < 0 || x >= p.vocab) {
-                    if (tid == 0) raise_flag(p.flags, MOE_FLAG_TOKEN);
-                } else if (x == token) {
-                    next = c;
-                    break;
-                }
-            }
-        } else {
-            double rest = 1.0;
-            bool fresh = false;      // s.part holds the weights at this S
-            for (int c = cur + 1; c < n; ++c) {
-                if ((p.parent ? p.parent[first + c] : c - 1) != cur) continue;
-                const int x = p.tokens[first + c];
-                if (x < 0 || x >= p.vocab) {
-                    if (tid == 0) raise_flag(p.flags, MOE_FLAG_TOKEN);
-                    continue;
-                }
-                if ((double)p.u_test[first + c] * (double)p.draft[qbase + x] * rest <
-                    weight<L>(r, p.logits, base, p.draft, qbase, x)) {
-                    next = c;
-                    token = x;
-                    break;
-                }
-                r.S += rest;
-                rest = sum_row<L>(r, p, base, qbase, s);
-                fresh = true;
-            }
-            if (next < 0) {
-                if (!(rest > 0.0)) { r.S = 0.0; fresh = false; }
-                if (!fresh) rest = sum_row<L>(r, p, base, qbase, s);
-                token = pick_row<L>(r, p, base, qbase, rest, p.u_pick[row], s);
-            }
-        }
-        if (tid == 0) {
-            r.S = 0.0;
-            p.path[first + kept - 1] = cur;
-            p.out_tokens[first + kept - 1] = token;
-            p.logprobs[first + kept - 1] = (float)log(target_weight<L>(r, p.logits, base, token));
-        }
-        if (next < 0) break;
-        cur = next;
-        ++kept;
-    }
-    if (tid == 0) p.n_keep[b] = kept;
-    for (int i = kept + tid; i < n; i += VERIFY_THREADS) {
-        p.path[first + i] = -1;
-        p.out_tokens[first + i] = -1;
-        p.logprobs[first + i] = 0.0f;
-    }
-}
-template __global__ void moe_verify_kernel<LogitF32>(VerifyParams);
-template __global__ void moe_verify_kernel<LogitBf16>(VerifyParams);
-template __global__ void moe_verify_kernel<LogitF16>(VerifyParams);
 
 }  // namespace moe

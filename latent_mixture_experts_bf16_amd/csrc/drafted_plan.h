@@ -44,6 +44,8 @@ constexpr int attend_blocks(int dim, int queries) {
     return dim <= 64 ? (queries == 16 ? 4 : 3) : dim <= 96 ? 3 : dim <= 128 ? 2 : 1;
 }
 
+constexpr int ATTEND_MOST_RANGES = 1024;
+
 // The first part of an item of attention work that was cut between workgroups: written by the range
 // that holds it, read by the launch that joins the parts.
 struct AttendPart {
@@ -60,15 +62,31 @@ struct AttendParams {
     float scale_log2;           // |scale| * log2(e), above 0: scores are exponents of 2
     int16_t q_sign;             // xor on the queries: the sign bit where the scale is negative
     int32_t rows, q_heads, group;
-    int32_t tile_queries;
+    int32_t tile_queries, ranges;
     AttendPart *parts;          // [ranges]
     float *part_stat;           // [2 ranges][2][tile_queries]: maximum, sum
     float *part_sum;            // [2 ranges][tile_queries][dim]
 };
 
 constexpr int MAX_VOCAB = 1 << 20;
-constexpr int VOCAB_CHUNK = 2048;   // logits per partial sum
-constexpr int MAX_CHUNKS = MAX_VOCAB / VOCAB_CHUNK;
+constexpr int VOCAB_CHUNK = 1024;   // logits of a row that one wave takes at a time
+
+// Of one chunk of a row, and of a whole row: the largest logit, its lowest index, and the sum of
+// exp((z - top) / T) (chunk) or 1 / that sum (row).
+struct LogitStat {
+    double sum;
+    float top;
+    int32_t best;               // -1: nothing above -infinity
+};
+
+// Where the walk of one sequence stands between launches.
+struct WalkState {
+    double S, rest;             // as moe_drafted.h names them
+    int32_t cur, kept, after;   // the row, the rows of the path so far, the last child that was tested
+    int32_t pending;            // 1: waits for the sum of max(p - S q, 0) over row cur
+    uint32_t done;              // workgroups that have added their part of it
+    uint32_t pad;
+};
 
 struct VerifyParams {
     const void *logits;
@@ -78,7 +96,14 @@ struct VerifyParams {
     int32_t *n_keep, *path, *out_tokens;
     float *logprobs;
     uint32_t *flags;
-    int32_t rows, seqs, vocab;
+    int32_t rows, seqs, vocab, chunks;
+    int32_t last_round;
+    LogitStat *chunk_stat;      // [rows][chunks]
+    LogitStat *row_stat;        // [rows]
+    double *token_p;            // [rows]: with draft_probs, p of the row's token at its parent; else log p of the pick
+    int32_t *pick;              // [rows]: without draft_probs, the token drawn after the row
+    double *left;               // [seqs][chunks]: sums of max(p - S q, 0)
+    WalkState *state;           // [seqs]
 };
 
 struct KeepParams {

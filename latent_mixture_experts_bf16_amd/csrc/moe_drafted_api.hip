@@ -12,7 +12,9 @@ namespace moe {
 template <bool F16, bool HALF, int W> __global__ void moe_rope_kernel(RopeParams p);
 template <bool F16, int D, int NQ, int QW> __global__ void moe_attend_kernel(AttendParams p);
 template <bool F16, int D> __global__ void moe_attend_join_kernel(AttendParams p);
-template <typename L> __global__ void moe_verify_kernel(VerifyParams p);
+template <typename L> __global__ void moe_verify_stats_kernel(VerifyParams p);
+template <typename L> __global__ void moe_verify_walk_kernel(VerifyParams p);
+template <typename L> __global__ void moe_verify_left_kernel(VerifyParams p);
 struct LogitF32;
 struct LogitBf16;
 struct LogitF16;
@@ -303,9 +305,9 @@ template <bool F16> static void attend_kernels(int dim, int queries, AttendKerne
 }
 
 // How the work is cut (the lengths are known on the device only): queries of a tile, ranges of
-// work, blocks along the queries of the launch that joins parts; and the workspace's layout.
+// work; and the workspace's layout.
 struct AttendShape {
-    int queries, ranges, join;
+    int queries, ranges;
     int64_t stat, sum, bytes;
 };
 static AttendShape attend_shape(const CacheParams &c, int32_t rows, int32_t q_heads) {
@@ -314,8 +316,8 @@ static AttendShape attend_shape(const CacheParams &c, int32_t rows, int32_t q_he
     // own numbers are on the device): a sequence with more of them reads its cache again.
     const int64_t mean = ((int64_t)rows * (q_heads / c.heads) + c.seqs - 1) / c.seqs;
     s.queries = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
+    static_assert(256 * attend_blocks(32, 16) <= ATTEND_MOST_RANGES, "");
     s.ranges = 256 * attend_blocks(c.dim, s.queries);     // as many workgroups as 256 compute units hold at once
-    s.join = mean <= 4 ? 1 : mean <= 16 ? 4 : 16;     // of four queries each
     s.stat = (int64_t)s.ranges * sizeof(AttendPart);
     s.sum = s.stat + (int64_t)s.ranges * 2 * 2 * s.queries * 4;
     s.bytes = s.sum + (int64_t)s.ranges * 2 * s.queries * c.dim * 4;
@@ -363,6 +365,7 @@ extern "C" int moe_tree_attend(const moe_paged_cache *c, int32_t rows, const voi
     p.q_heads = q_heads;
     p.group = q_heads / p.c.heads;
     p.tile_queries = shape.queries;
+    p.ranges = shape.ranges;
     p.parts = (AttendPart *)workspace;
     p.part_stat = (float *)((char *)workspace + shape.stat);
     p.part_sum = (float *)((char *)workspace + shape.sum);
@@ -372,7 +375,7 @@ extern "C" int moe_tree_attend(const moe_paged_cache *c, int32_t rows, const voi
     else
         attend_kernels<false>(p.c.dim, shape.queries, &main, &join);
     if ((rc = launch("tree_attend", main, dim3((unsigned)shape.ranges), dim3(256), p, hip_stream))) return rc;
-    return launch("tree_attend join", join, dim3((unsigned)shape.ranges, (unsigned)shape.join), dim3(256), p, hip_stream);
+    return launch("tree_attend join", join, dim3(512), dim3(256), p, hip_stream);
 }
 
 // ------------------------------------------------------------------ draft verification
@@ -385,10 +388,52 @@ static int check_verify_sizes(int64_t rows, int32_t seqs, int64_t vocab) {
     return MOE_OK;
 }
 
+// Bytes of workspace; with a base and p, also its parts.
+static int64_t verify_layout(int64_t rows, int64_t seqs, int64_t vocab, char *base, VerifyParams *p) {
+    const int64_t chunks = (vocab + VOCAB_CHUNK - 1) / VOCAB_CHUNK;
+    const int64_t row_stat = rows * chunks * (int64_t)sizeof(LogitStat);
+    const int64_t state = row_stat + rows * (int64_t)sizeof(LogitStat);
+    const int64_t left = state + seqs * (int64_t)sizeof(WalkState);
+    const int64_t token_p = left + seqs * chunks * 8;
+    const int64_t pick = token_p + rows * 8;
+    if (p) {
+        p->chunks = (int32_t)chunks;
+        p->chunk_stat = (LogitStat *)base;
+        p->row_stat = (LogitStat *)(base + row_stat);
+        p->state = (WalkState *)(base + state);
+        p->left = (double *)(base + left);
+        p->token_p = (double *)(base + token_p);
+        p->pick = (int32_t *)(base + pick);
+    }
+    return pick + rows * 4;
+}
+
 extern "C" int64_t moe_draft_verify_workspace(int32_t rows, int32_t seqs, int32_t vocab) {
     api_clear();
     const int rc = check_verify_sizes(rows, seqs, vocab);
-    return rc ? -rc : 0;
+    return rc ? -rc : verify_layout(rows, seqs, vocab, nullptr, nullptr);
+}
+
+// Tests of whole rows that are launched before the last one, whose own workgroups take what is left: a chain
+// never needs a second one. An empty one costs a launch (about 3 us), one too few a row summed by a
+// single workgroup.
+constexpr int TREE_ROUNDS = 3;
+
+template <typename L> static int verify_launches(VerifyParams &p, void *stream) {
+    int rc;
+    const unsigned y = (unsigned)(p.rows < 32768 ? p.rows : 32768);
+    if ((rc = launch("draft_verify", moe_verify_stats_kernel<L>,
+                     dim3((unsigned)(p.chunks + 3) / 4, y, ((unsigned)p.rows + y - 1) / y), dim3(256), p, stream)) ||
+        (rc = launch("draft_verify walk", moe_verify_walk_kernel<L>, dim3((unsigned)p.seqs), dim3(512), p, stream)))
+        return rc;
+    const int rounds = !p.draft ? 0 : p.parent ? TREE_ROUNDS : 1;
+    for (int i = 0; i < rounds; ++i) {
+        p.last_round = i == rounds - 1;
+        if ((rc = launch("draft_verify left", moe_verify_left_kernel<L>,
+                         dim3((unsigned)p.seqs, (unsigned)(p.chunks + 15) / 16), dim3(1024), p, stream)))
+            return rc;
+    }
+    return MOE_OK;
 }
 
 extern "C" int moe_draft_verify(const moe_tensor *logits, const int32_t *tokens, const int32_t *row_start,
@@ -423,7 +468,9 @@ extern "C" int moe_draft_verify(const moe_tensor *logits, const int32_t *tokens,
             return api_fail(MOE_ERR_LAYOUT, "draft_probs: row stride %lld, %lld wide", (long long)draft_stride,
                             (long long)vocab);
     }
-    if ((rc = device_cus(&cus))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, verify_layout(rows, seqs, vocab, nullptr, nullptr))) ||
+        (rc = device_cus(&cus)))
+        return rc;
     VerifyParams p;
     memset(&p, 0, sizeof p);
     p.logits = logits->data;
@@ -444,12 +491,10 @@ extern "C" int moe_draft_verify(const moe_tensor *logits, const int32_t *tokens,
     p.rows = (int32_t)rows;
     p.seqs = seqs;
     p.vocab = (int32_t)vocab;
-    (void)workspace;
-    (void)workspace_bytes;
-    void (*kern)(VerifyParams) = logits->dtype == MOE_DT_F32    ? moe_verify_kernel<LogitF32>
-                                 : logits->dtype == MOE_DT_BF16 ? moe_verify_kernel<LogitBf16>
-                                                                : moe_verify_kernel<LogitF16>;
-    return launch("draft_verify", kern, dim3((unsigned)seqs), dim3(1024), p, hip_stream);
+    verify_layout(rows, seqs, vocab, (char *)workspace, &p);
+    return logits->dtype == MOE_DT_F32    ? verify_launches<LogitF32>(p, hip_stream)
+           : logits->dtype == MOE_DT_BF16 ? verify_launches<LogitBf16>(p, hip_stream)
+                                          : verify_launches<LogitF16>(p, hip_stream);
 }
 
 // ------------------------------------------------------------------ path keeping

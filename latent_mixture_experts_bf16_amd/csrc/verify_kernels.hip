@@ -1,0 +1,399 @@
+// verify_kernels.hip -- verification of drafted tokens against the target's probabilities (gfx950).
+//
+// Probabilities and their running sums decide which whole token comes out, so they are held in
+// 64 bits throughout: a running sum over 10^5 terms in 32 bits is off by more than the probability
+// of most tokens.
+//
+//   stats  every row's logits once, a wave per chunk of 1024: largest, its index, sum of exponentials.
+//          The walk needs the path's rows only, but does not know them before it has their sums, and one
+//          row after another would leave most of the card idle.
+//   walk   a workgroup per sequence: its rows' chunks joined, a wave a row; without draft
+//          probabilities also each row's pick, after which the walk itself only compares tokens; with
+//          them the drafted tokens' probabilities, after which it needs a whole row again only where a
+//          draft is refused (the sum of max(p - S q, 0)) -- there it stops and leaves its state.
+//   left   that sum, for all sequences that stopped, a wave per chunk; the last workgroup of a
+//          sequence to finish goes on with its walk. A chain needs it once. Trees, whose later
+//          siblings may be refused too, get it a few times; what then still waits is summed by the
+//          last launch's own workgroup.
+#include "drafted_items.h"
+
+namespace moe {
+
+struct LogitF32 {
+    typedef float T;
+    static __device__ __forceinline__ float value(float v) { return v; }
+};
+struct LogitBf16 {
+    typedef uint16_t T;
+    static __device__ __forceinline__ float value(uint16_t v) { return bf2f(v); }
+};
+struct LogitF16 {
+    typedef uint16_t T;
+    static __device__ __forceinline__ float value(uint16_t v) { return h2f(v); }
+};
+
+__device__ __forceinline__ double wave_sum(double v) {
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+    return v;
+}
+__device__ __forceinline__ double wave_scan(double v) {     // inclusive
+    for (int d = 1; d < 64; d <<= 1) {
+        const double u = __shfl_up(v, d);
+        if (lane_id() >= d) v += u;
+    }
+    return v;
+}
+
+// A lane's share of a chunk: four times four neighbours, 256 apart; rows start anywhere, so the
+// loads are of the element's alignment.
+constexpr int SHARE = VOCAB_CHUNK / 64;
+__device__ __forceinline__ int share_index(int k) { return (k >> 2) * 256 + lane_id() * 4 + (k & 3); }
+
+template <typename T> struct __attribute__((packed)) Four {
+    T v[4];
+};
+
+// The share of chunk c of a row; past the vocabulary `fill`.
+template <typename L, typename F>
+__device__ __forceinline__ void load_share(const typename L::T *row, int c, int vocab, float fill, F *x) {
+    const int base = c * VOCAB_CHUNK;
+    if (base + VOCAB_CHUNK <= vocab) {
+#pragma unroll
+        for (int k = 0; k < SHARE; k += 4) {
+            const Four<typename L::T> f = *(const Four<typename L::T> *)(row + base + share_index(k));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[k + e] = L::value(f.v[e]);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < SHARE; ++k) {
+            const int i = base + share_index(k);
+            x[k] = i < vocab ? L::value(row[i]) : fill;
+        }
+    }
+}
+
+// Temperature of a sequence: 1 / T, and whether all weight is on the largest logit. (An infinite T
+// counts as the largest finite one, so that a logit of -infinity still weighs nothing.)
+struct Heat {
+    double inv;
+    bool greedy;
+};
+__device__ __forceinline__ Heat heat(const VerifyParams &p, int b) {
+    const float T = p.temperature ? p.temperature[b] : 1.0f;
+    return {1.0 / (double)fminf(T, 3.4028234e38f), !(T > 0.0f)};
+}
+
+// exp((x - top) / T). Equal first: the largest may be infinite; NaN compares false and weighs nothing.
+__device__ __forceinline__ double relative(float x, float top, double inv_t) {
+    const double e = exp(((double)x - (double)top) * inv_t);
+    return x == top ? 1.0 : x < top ? e : 0.0;
+}
+
+// p of index i with logit x in a row whose statistics are r.
+__device__ __forceinline__ double target(const LogitStat &r, const Heat &h, int i, float x) {
+    if (h.greedy || r.best < 0) return i == max(r.best, 0) ? 1.0 : 0.0;
+    return relative(x, r.top, h.inv) * r.sum;
+}
+
+template <typename L> __device__ __forceinline__ const typename L::T *logits_of(const VerifyParams &p, int row) {
+    return (const typename L::T *)p.logits + (int64_t)row * p.logit_stride;
+}
+
+// ------------------------------------------------------------------ stats
+
+template <typename L> __global__ void __launch_bounds__(256) moe_verify_stats_kernel(VerifyParams p) {
+    const int row = (int)(blockIdx.z * gridDim.y + blockIdx.y), lane = lane_id();
+    const int c = (int)blockIdx.x * 4 + uniform((int)threadIdx.x >> 6);
+    if (row >= p.rows || c >= p.chunks) return;
+    float x[SHARE];
+    load_share<L>(logits_of<L>(p, row), c, p.vocab, -__builtin_inff(), x);
+    int first = 0;
+    // a row of no sequence is not walked; but where row_start is not ascending the walk may read it all the same
+    const int b = seq_of_row(p.row_start, p.seqs, row, &first);
+    const Heat h = b < 0 ? Heat{1.0, false} : heat(p, b);
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int k = 0; k < SHARE; ++k) top = fmaxf(top, x[k]);      // not a NaN: the other operand
+    for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    int best = -1;
+    double sum = 0.0;
+    if (top > -__builtin_inff()) {
+        // the lowest index: the first quarter of the chunk that has the value, its first lane, that lane's first
+#pragma unroll
+        for (int k = SHARE - 4; k >= 0; k -= 4) {
+            int at = 4;
+#pragma unroll
+            for (int e = 3; e >= 0; --e) at = x[k + e] == top ? e : at;
+            const uint64_t some = __ballot(at < 4);
+            if (some) {
+                const int l = __builtin_ctzll(some);
+                best = c * VOCAB_CHUNK + (k >> 2) * 256 + l * 4 + __shfl(at, l);
+            }
+        }
+        if (!h.greedy) {
+#pragma unroll
+            for (int k = 0; k < SHARE; ++k) sum += relative(x[k], top, h.inv);
+            sum = wave_sum(sum);
+        }
+    }
+    if (lane == 0) p.chunk_stat[(int64_t)row * p.chunks + c] = LogitStat{sum, top, best};
+}
+
+// ------------------------------------------------------------------ picking
+
+// Statistics of a whole row from its chunks, the same in every lane.
+__device__ __forceinline__ LogitStat join_chunks(const VerifyParams &p, const Heat &h, int row) {
+    const LogitStat *s = p.chunk_stat + (int64_t)row * p.chunks;
+    LogitStat r = {0.0, -__builtin_inff(), -1};
+    for (int c = lane_id(); c < p.chunks; c += 64)
+        if (s[c].top > r.top) { r.top = s[c].top; r.best = s[c].best; }
+    for (int d = 32; d; d >>= 1) {
+        const float t = __shfl_xor(r.top, d);
+        const int i = __shfl_xor(r.best, d);
+        if (i >= 0 && (t > r.top || (t == r.top && i < r.best))) { r.top = t; r.best = i; }
+    }
+    if (r.best < 0 || h.greedy) return r;
+    for (int c = lane_id(); c < p.chunks; c += 64) r.sum += s[c].sum * relative(s[c].top, r.top, h.inv);
+    r.sum = 1.0 / wave_sum(r.sum);
+    return r;
+}
+
+// The first index of row `row` whose running sum of weights passes u times the whole sum: of p where S is 0, else of
+// max(p - S q, 0), whose sums by chunk are in p.left. By one wave.
+template <typename L>
+__device__ int pick_token(const VerifyParams &p, const LogitStat &r, const Heat &h, int b, int row, double S, float u) {
+    if (S == 0.0 && (h.greedy || r.best < 0)) return max(r.best, 0);
+    const LogitStat *s = p.chunk_stat + (int64_t)row * p.chunks;
+    const double *left = p.left + (int64_t)b * p.chunks;
+    const int lane = lane_id();
+    auto chunk_weight = [&](int c) {
+        if (c >= p.chunks) return 0.0;
+        return S > 0.0 ? left[c] : s[c].best < 0 ? 0.0 : s[c].sum * relative(s[c].top, r.top, h.inv) * r.sum;
+    };
+    double total = 0.0;
+    for (int c0 = 0; c0 < p.chunks; c0 += 64) total += wave_sum(chunk_weight(c0 + lane));
+    const double goal = (double)u * total;
+    // the chunk: the first whose running sum passes, or (a last rounding) the last with weight
+    int chunk = -1;
+    double run = 0.0, before = 0.0;
+    for (int c0 = 0; c0 < p.chunks; c0 += 64) {
+        const double w = chunk_weight(c0 + lane), cum = run + wave_scan(w);
+        const uint64_t some = __ballot(w > 0.0), past = __ballot(w > 0.0 && cum > goal);
+        if (past || some) {
+            const int l = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some);
+            chunk = c0 + l;
+            before = __shfl(cum - w, l);
+        }
+        if (past) break;
+        run = __shfl(cum, 63);
+    }
+    if (chunk < 0) return 0;
+    // the same within it
+    float x[SHARE], q[SHARE];
+    load_share<L>(logits_of<L>(p, row), chunk, p.vocab, -__builtin_inff(), x);
+    if (S > 0.0) load_share<LogitF32>(p.draft + (int64_t)row * p.draft_stride, chunk, p.vocab, 0.0f, q);
+    int found = -1;
+    run = before;
+#pragma unroll
+    for (int k = 0; k < SHARE; k += 4) {
+        double w[4], mine = 0.0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = chunk * VOCAB_CHUNK + share_index(k + e);
+            w[e] = i < p.vocab ? target(r, h, i, x[k + e]) : 0.0;
+            if (S > 0.0) w[e] = fmax(w[e] - S * (double)q[k + e], 0.0);
+            mine += w[e];
+        }
+        const double upto = run + wave_scan(mine);
+        double cum = upto - mine;
+        int first = -1, last = -1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            cum += w[e];
+            if (w[e] > 0.0) last = e;
+            if (w[e] > 0.0 && cum > goal && first < 0) first = e;
+        }
+        const uint64_t past = __ballot(first >= 0), some = __ballot(last >= 0);
+        const int l = past ? __builtin_ctzll(past) : some ? 63 - __builtin_clzll(some) : 0;
+        const int e = __shfl(past ? first : last, l);
+        if (past || some) found = chunk * VOCAB_CHUNK + (k >> 2) * 256 + l * 4 + e;
+        if (past) break;
+        run = __shfl(upto, 63);
+    }
+    return max(found, 0);
+}
+
+// ------------------------------------------------------------------ the walk
+
+// Chunk c of max(p - S q, 0) over a row, summed by one wave.
+template <typename L>
+__device__ __forceinline__ double left_of_chunk(const VerifyParams &p, const LogitStat &r, const Heat &h, int row, int c,
+                                                double S) {
+    float x[SHARE], q[SHARE];
+    load_share<L>(logits_of<L>(p, row), c, p.vocab, -__builtin_inff(), x);
+    load_share<LogitF32>(p.draft + (int64_t)row * p.draft_stride, c, p.vocab, 0.0f, q);
+    double sum = 0.0;
+#pragma unroll
+    for (int k = 0; k < SHARE; ++k)
+        sum += fmax(target(r, h, c * VOCAB_CHUNK + share_index(k), x[k]) - S * (double)q[k], 0.0);
+    return wave_sum(sum);
+}
+
+// One wave walks on from st. true: the sequence is done; false: st waits for the sum of max(p - S q, 0).
+template <typename L>
+__device__ bool walk(const VerifyParams &p, const Heat &h, int b, int first, int n, WalkState &st) {
+    const int lane = lane_id();
+    for (;;) {
+        const int row = first + st.cur;
+        // without draft probabilities the token is known, and only a child that holds it counts
+        const int drawn = p.draft ? -1 : p.pick[row];
+        int kid = -1, token = -1;
+        for (int c0 = (st.after + 1) & ~63; c0 < n && kid < 0; c0 += 64) {
+            const int c = c0 + lane;
+            const bool is = c > st.after && c < n && (p.parent ? p.parent[first + c] : c - 1) == st.cur;
+            const int x = is ? p.tokens[first + c] : 0;
+            const bool bad = is && (x < 0 || x >= p.vocab);
+            const uint64_t fits = __ballot(is && !bad && (p.draft || x == drawn)), wrong = __ballot(bad);
+            if (fits) {
+                const int l = __builtin_ctzll(fits);
+                kid = c0 + l;
+                token = __shfl(x, l);
+            }
+            if (wrong && (!fits || __builtin_ctzll(wrong) < __builtin_ctzll(fits)) && lane == 0)
+                raise_flag(p.flags, MOE_FLAG_TOKEN);
+        }
+        if (p.row_stat[row].best < 0 && lane == 0) raise_flag(p.flags, MOE_FLAG_LOGITS);
+        double lp;
+        if (!p.draft) {
+            token = drawn;
+            lp = p.token_p[row];
+        } else if (kid >= 0) {
+            const double px = p.token_p[first + kid];
+            const double qx = (double)p.draft[(int64_t)row * p.draft_stride + token];
+            if (!((double)p.u_test[first + kid] * qx * st.rest < fmax(px - st.S * qx, 0.0))) {
+                st.S += st.rest;
+                st.after = kid;
+                return false;
+            }
+            lp = log(px);
+        } else {
+            const LogitStat r = p.row_stat[row];
+            token = pick_token<L>(p, r, h, b, row, st.rest > 0.0 ? st.S : 0.0, p.u_pick[row]);
+            lp = log(target(r, h, token, L::value(logits_of<L>(p, row)[token])));
+        }
+        if (lane == 0) {
+            p.path[first + st.kept - 1] = st.cur;
+            p.out_tokens[first + st.kept - 1] = token;
+            p.logprobs[first + st.kept - 1] = (float)lp;
+        }
+        if (kid < 0) break;
+        st.cur = st.after = kid;
+        st.S = 0.0;
+        st.rest = 1.0;
+        ++st.kept;
+    }
+    if (lane == 0) p.n_keep[b] = st.kept;
+    for (int i = st.kept + lane; i < n; i += 64) {
+        p.path[first + i] = -1;
+        p.out_tokens[first + i] = -1;
+        p.logprobs[first + i] = 0.0f;
+    }
+    return true;
+}
+
+template <typename L> __global__ void __launch_bounds__(512) moe_verify_walk_kernel(VerifyParams p) {
+    const int b = (int)blockIdx.x, tid = (int)threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
+    int first = 0;
+    const int n = seq_rows(p.row_start, b, p.rows, &first, p.flags);
+    WalkState &out = p.state[b];
+    if (n == 0) {
+        if (tid == 0) {
+            p.n_keep[b] = 0;
+            out.pending = 0;
+        }
+        return;
+    }
+    const Heat h = heat(p, b);
+    for (int i = wave; i < n; i += 8) {
+        const int row = first + i;
+        const LogitStat r = join_chunks(p, h, row);
+        if (lane == 0) p.row_stat[row] = r;
+        if (!p.draft) {
+            const int t = pick_token<L>(p, r, h, b, row, 0.0, p.u_pick[row]);
+            if (lane == 0) {
+                p.pick[row] = t;
+                p.token_p[row] = log(target(r, h, t, L::value(logits_of<L>(p, row)[t])));
+            }
+        }
+    }
+    __syncthreads();
+    if (p.draft) {
+        for (int c = 1 + tid; c < n; c += 512) {
+            const int par = p.parent ? p.parent[first + c] : c - 1, x = p.tokens[first + c];
+            if (par >= 0 && par < c && x >= 0 && x < p.vocab)
+                p.token_p[first + c] = target(p.row_stat[first + par], h, x, L::value(logits_of<L>(p, first + par)[x]));
+        }
+        __syncthreads();
+    }
+    if (wave == 0) {
+        WalkState st = {0.0, 1.0, 0, 1, 0, 0, 0, 0};
+        st.pending = !walk<L>(p, h, b, first, n, st);
+        if (lane == 0) out = st;
+    }
+}
+
+// Workgroup (b, y): sums of 16 chunks of sequence b's row, if it waits for them.
+template <typename L> __global__ void __launch_bounds__(1024) moe_verify_left_kernel(VerifyParams p) {
+    __shared__ int ours;
+    const int b = (int)blockIdx.x, part = (int)blockIdx.y, tid = (int)threadIdx.x, lane = lane_id();
+    const int wave = uniform(tid >> 6);
+    WalkState st = p.state[b];
+    if (!st.pending) return;
+    const int first = uniform(p.row_start[b]), n = uniform(p.row_start[b + 1]) - first;     // checked by the walk
+    const Heat h = heat(p, b);
+    double *left = p.left + (int64_t)b * p.chunks;
+    const int c = part * 16 + wave;
+    if (c < p.chunks) {
+        const double s = left_of_chunk<L>(p, p.row_stat[first + st.cur], h, first + st.cur, c, st.S);
+        if (lane == 0) left[c] = s;
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) ours = atomicAdd(&p.state[b].done, 1u) + 1 == gridDim.y;
+    __syncthreads();
+    if (!ours) return;
+    __threadfence();
+    for (;;) {
+        if (wave == 0) {
+            double sum = 0.0;
+            for (int k = lane; k < p.chunks; k += 64) sum += left[k];
+            st.rest = wave_sum(sum);
+            st.pending = !walk<L>(p, h, b, first, n, st);
+            if (lane == 0) {
+                st.done = 0;
+                p.state[b] = st;
+            }
+        }
+        if (!p.last_round) return;
+        __syncthreads();
+        st = p.state[b];
+        __syncthreads();
+        if (!st.pending) return;
+        for (int k = wave; k < p.chunks; k += 16) {
+            const double s = left_of_chunk<L>(p, p.row_stat[first + st.cur], h, first + st.cur, k, st.S);
+            if (lane == 0) left[k] = s;
+        }
+        __syncthreads();
+    }
+}
+
+#define VERIFY_KERNELS(L)                                            \
+    template __global__ void moe_verify_stats_kernel<L>(VerifyParams); \
+    template __global__ void moe_verify_walk_kernel<L>(VerifyParams);  \
+    template __global__ void moe_verify_left_kernel<L>(VerifyParams)
+VERIFY_KERNELS(LogitF32);
+VERIFY_KERNELS(LogitBf16);
+VERIFY_KERNELS(LogitF16);
+
+}  // namespace moe
