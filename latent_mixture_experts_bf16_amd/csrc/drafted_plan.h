@@ -100,7 +100,7 @@ struct VerifyParams {
     int32_t last_round;
     LogitStat *chunk_stat;      // [rows][chunks]
     LogitStat *row_stat;        // [rows]
-    double *token_p;            // [rows]: with draft_probs, p of the row's token at its parent; else log p of the pick
+    double *token_p;            // [rows]: without draft_probs, log p of the pick
     int32_t *pick;              // [rows]: without draft_probs, the token drawn after the row
     double *left;               // [seqs][chunks]: sums of max(p - S q, 0)
     WalkState *state;           // [seqs]

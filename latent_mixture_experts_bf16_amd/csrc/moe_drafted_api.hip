@@ -424,7 +424,7 @@ template <typename L> static int verify_launches(VerifyParams &p, void *stream) 
     const unsigned y = (unsigned)(p.rows < 32768 ? p.rows : 32768);
     if ((rc = launch("draft_verify", moe_verify_stats_kernel<L>,
                      dim3((unsigned)(p.chunks + 3) / 4, y, ((unsigned)p.rows + y - 1) / y), dim3(256), p, stream)) ||
-        (rc = launch("draft_verify walk", moe_verify_walk_kernel<L>, dim3((unsigned)p.seqs), dim3(512), p, stream)))
+        (rc = launch("draft_verify walk", moe_verify_walk_kernel<L>, dim3((unsigned)p.seqs), dim3(1024), p, stream)))
         return rc;
     const int rounds = !p.draft ? 0 : p.parent ? TREE_ROUNDS : 1;
     for (int i = 0; i < rounds; ++i) {

@@ -44,6 +44,15 @@ __device__ __forceinline__ double wave_scan(double v) {     // inclusive
     return v;
 }
 
+// The sums of max(p - S q, 0) are read by another workgroup of the same launch: written through to memory and read
+// around the caches, as layer_items.h does for smaller types.
+__device__ __forceinline__ void st_shared64(double *p, double v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ double ld_shared64(const double *p) {
+    return __hip_atomic_load(const_cast<double *>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // A lane's share of a chunk: four times four neighbours, 256 apart; rows start anywhere, so the
 // loads are of the element's alignment.
 constexpr int SHARE = VOCAB_CHUNK / 64;
@@ -169,7 +178,7 @@ __device__ int pick_token(const VerifyParams &p, const LogitStat &r, const Heat 
     const int lane = lane_id();
     auto chunk_weight = [&](int c) {
         if (c >= p.chunks) return 0.0;
-        return S > 0.0 ? left[c] : s[c].best < 0 ? 0.0 : s[c].sum * relative(s[c].top, r.top, h.inv) * r.sum;
+        return S > 0.0 ? ld_shared64(left + c) : s[c].best < 0 ? 0.0 : s[c].sum * relative(s[c].top, r.top, h.inv) * r.sum;
     };
     double total = 0.0;
     for (int c0 = 0; c0 < p.chunks; c0 += 64) total += wave_sum(chunk_weight(c0 + lane));
@@ -240,54 +249,97 @@ __device__ __forceinline__ double left_of_chunk(const VerifyParams &p, const Log
     return wave_sum(sum);
 }
 
+// 64 rows of a sequence, one a lane: as children, and (without draft probabilities) their own picks.
+struct Kids {
+    int parent, token, drawn;   // token -1: outside the vocabulary
+    double p, lp;               // p of the token at its parent; its log, or that of the row's own pick
+    float q, u;
+    bool empty;                 // the parent's row (or the row itself, without draft probabilities) holds no logit
+};
+template <typename L>
+__device__ __forceinline__ Kids load_kids(const VerifyParams &p, const Heat &h, int first, int n, int c) {
+    Kids k = {-1, -1, -1, 0.0, 0.0, 0.0f, 0.0f, false};
+    if (c >= n) return k;
+    k.parent = c == 0 ? -1 : p.parent ? p.parent[first + c] : c - 1;
+    const int x = p.tokens[first + c];
+    if (c && x >= 0 && x < p.vocab) k.token = x;
+    if (!p.draft) {
+        k.drawn = p.pick[first + c];
+        k.lp = p.token_p[first + c];
+        k.empty = p.row_stat[first + c].best < 0;
+    } else if (k.parent >= 0 && k.parent < c && k.token >= 0) {
+        const int row = first + k.parent;
+        const LogitStat r = p.row_stat[row];
+        k.p = target(r, h, x, L::value(logits_of<L>(p, row)[x]));
+        k.lp = log(k.p);
+        k.q = p.draft[(int64_t)row * p.draft_stride + x];
+        k.u = p.u_test[first + c];
+        k.empty = r.best < 0;
+    }
+    return k;
+}
+
 // One wave walks on from st. true: the sequence is done; false: st waits for the sum of max(p - S q, 0).
 template <typename L>
 __device__ bool walk(const VerifyParams &p, const Heat &h, int b, int first, int n, WalkState &st) {
     const int lane = lane_id();
+    int have = (st.after + 1) & ~63;
+    if (have >= n) have = (n - 1) & ~63;
+    Kids k = load_kids<L>(p, h, first, n, have + lane);
+    // without draft probabilities the walk is not interrupted: it starts at row 0, in lane 0
+    int drawn = __shfl(k.drawn, 0);
+    double drawn_lp = __shfl(k.lp, 0);
+    bool drawn_empty = __shfl((int)k.empty, 0);
     for (;;) {
         const int row = first + st.cur;
-        // without draft probabilities the token is known, and only a child that holds it counts
-        const int drawn = p.draft ? -1 : p.pick[row];
-        int kid = -1, token = -1;
-        for (int c0 = (st.after + 1) & ~63; c0 < n && kid < 0; c0 += 64) {
-            const int c = c0 + lane;
-            const bool is = c > st.after && c < n && (p.parent ? p.parent[first + c] : c - 1) == st.cur;
-            const int x = is ? p.tokens[first + c] : 0;
-            const bool bad = is && (x < 0 || x >= p.vocab);
-            const uint64_t fits = __ballot(is && !bad && (p.draft || x == drawn)), wrong = __ballot(bad);
-            if (fits) {
-                const int l = __builtin_ctzll(fits);
-                kid = c0 + l;
-                token = __shfl(x, l);
-            }
+        int kid = -1;
+        for (int c0 = (st.after + 1) & ~63; c0 < n; c0 += 64) {
+            if (c0 != have) k = load_kids<L>(p, h, first, n, c0 + lane);
+            have = c0;
+            const bool is = c0 + lane > st.after && k.parent == st.cur;
+            const uint64_t fits = __ballot(is && k.token >= 0 && (p.draft || k.token == drawn));
+            const uint64_t wrong = __ballot(is && k.token < 0);
             if (wrong && (!fits || __builtin_ctzll(wrong) < __builtin_ctzll(fits)) && lane == 0)
                 raise_flag(p.flags, MOE_FLAG_TOKEN);
+            if (fits) {
+                kid = c0 + __builtin_ctzll(fits);
+                break;
+            }
         }
-        if (p.row_stat[row].best < 0 && lane == 0) raise_flag(p.flags, MOE_FLAG_LOGITS);
+        const int l = kid & 63;
+        int token;
         double lp;
+        bool empty;
         if (!p.draft) {
             token = drawn;
-            lp = p.token_p[row];
+            lp = drawn_lp;
+            empty = drawn_empty;
         } else if (kid >= 0) {
-            const double px = p.token_p[first + kid];
-            const double qx = (double)p.draft[(int64_t)row * p.draft_stride + token];
-            if (!((double)p.u_test[first + kid] * qx * st.rest < fmax(px - st.S * qx, 0.0))) {
+            const double px = __shfl(k.p, l), qx = (double)__shfl(k.q, l);
+            if (!((double)__shfl(k.u, l) * qx * st.rest < fmax(px - st.S * qx, 0.0))) {
                 st.S += st.rest;
                 st.after = kid;
                 return false;
             }
-            lp = log(px);
+            token = __shfl(k.token, l);
+            lp = __shfl(k.lp, l);
+            empty = __shfl((int)k.empty, l);
         } else {
             const LogitStat r = p.row_stat[row];
             token = pick_token<L>(p, r, h, b, row, st.rest > 0.0 ? st.S : 0.0, p.u_pick[row]);
             lp = log(target(r, h, token, L::value(logits_of<L>(p, row)[token])));
+            empty = r.best < 0;
         }
         if (lane == 0) {
             p.path[first + st.kept - 1] = st.cur;
             p.out_tokens[first + st.kept - 1] = token;
             p.logprobs[first + st.kept - 1] = (float)lp;
+            if (empty) raise_flag(p.flags, MOE_FLAG_LOGITS);
         }
         if (kid < 0) break;
+        drawn = __shfl(k.drawn, l);
+        drawn_lp = __shfl(k.lp, l);
+        drawn_empty = __shfl((int)k.empty, l);
         st.cur = st.after = kid;
         st.S = 0.0;
         st.rest = 1.0;
@@ -302,7 +354,7 @@ __device__ bool walk(const VerifyParams &p, const Heat &h, int b, int first, int
     return true;
 }
 
-template <typename L> __global__ void __launch_bounds__(512) moe_verify_walk_kernel(VerifyParams p) {
+template <typename L> __global__ void __launch_bounds__(1024) moe_verify_walk_kernel(VerifyParams p) {
     const int b = (int)blockIdx.x, tid = (int)threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
     int first = 0;
     const int n = seq_rows(p.row_start, b, p.rows, &first, p.flags);
@@ -315,7 +367,7 @@ template <typename L> __global__ void __launch_bounds__(512) moe_verify_walk_ker
         return;
     }
     const Heat h = heat(p, b);
-    for (int i = wave; i < n; i += 8) {
+    for (int i = wave; i < n; i += 16) {
         const int row = first + i;
         const LogitStat r = join_chunks(p, h, row);
         if (lane == 0) p.row_stat[row] = r;
@@ -328,14 +380,6 @@ template <typename L> __global__ void __launch_bounds__(512) moe_verify_walk_ker
         }
     }
     __syncthreads();
-    if (p.draft) {
-        for (int c = 1 + tid; c < n; c += 512) {
-            const int par = p.parent ? p.parent[first + c] : c - 1, x = p.tokens[first + c];
-            if (par >= 0 && par < c && x >= 0 && x < p.vocab)
-                p.token_p[first + c] = target(p.row_stat[first + par], h, x, L::value(logits_of<L>(p, first + par)[x]));
-        }
-        __syncthreads();
-    }
     if (wave == 0) {
         WalkState st = {0.0, 1.0, 0, 1, 0, 0, 0, 0};
         st.pending = !walk<L>(p, h, b, first, n, st);
@@ -346,8 +390,8 @@ template <typename L> __global__ void __launch_bounds__(512) moe_verify_walk_ker
 // Workgroup (b, y): sums of 16 chunks of sequence b's row, if it waits for them.
 template <typename L> __global__ void __launch_bounds__(1024) moe_verify_left_kernel(VerifyParams p) {
     __shared__ int ours;
-    const int b = (int)blockIdx.x, part = (int)blockIdx.y, tid = (int)threadIdx.x, lane = lane_id();
-    const int wave = uniform(tid >> 6);
+    const int b = (int)blockIdx.x, part = (int)blockIdx.y, lane = lane_id();
+    const int wave = uniform((int)threadIdx.x >> 6);
     WalkState st = p.state[b];
     if (!st.pending) return;
     const int first = uniform(p.row_start[b]), n = uniform(p.row_start[b + 1]) - first;     // checked by the walk
@@ -356,24 +400,16 @@ template <typename L> __global__ void __launch_bounds__(1024) moe_verify_left_ke
     const int c = part * 16 + wave;
     if (c < p.chunks) {
         const double s = left_of_chunk<L>(p, p.row_stat[first + st.cur], h, first + st.cur, c, st.S);
-        if (lane == 0) left[c] = s;
+        if (lane == 0) st_shared64(left + c, s);
     }
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) ours = atomicAdd(&p.state[b].done, 1u) + 1 == gridDim.y;
-    __syncthreads();
-    if (!ours) return;
-    __threadfence();
+    if (!last_arriver(&p.state[b].done, gridDim.y, &ours)) return;
     for (;;) {
         if (wave == 0) {
             double sum = 0.0;
-            for (int k = lane; k < p.chunks; k += 64) sum += left[k];
+            for (int k = lane; k < p.chunks; k += 64) sum += ld_shared64(left + k);
             st.rest = wave_sum(sum);
             st.pending = !walk<L>(p, h, b, first, n, st);
-            if (lane == 0) {
-                st.done = 0;
-                p.state[b] = st;
-            }
+            if (lane == 0) p.state[b] = st;
         }
         if (!p.last_round) return;
         __syncthreads();
@@ -382,8 +418,9 @@ template <typename L> __global__ void __launch_bounds__(1024) moe_verify_left_ke
         if (!st.pending) return;
         for (int k = wave; k < p.chunks; k += 16) {
             const double s = left_of_chunk<L>(p, p.row_stat[first + st.cur], h, first + st.cur, k, st.S);
-            if (lane == 0) left[k] = s;
+            if (lane == 0) st_shared64(left + k, s);
         }
+        wait_vmem();
         __syncthreads();
     }
 }
