@@ -430,7 +430,7 @@ template <typename L> static int verify_launches(VerifyParams &p, void *stream) 
     for (int i = 0; i < rounds; ++i) {
         p.last_round = i == rounds - 1;
         if ((rc = launch("draft_verify left", moe_verify_left_kernel<L>,
-                         dim3((unsigned)p.seqs, (unsigned)(p.chunks + 15) / 16), dim3(1024), p, stream)))
+                         dim3((unsigned)p.seqs, (unsigned)(p.chunks + 7) / 8), dim3(512), p, stream)))
             return rc;
     }
     return MOE_OK;

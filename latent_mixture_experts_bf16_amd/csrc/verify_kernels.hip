@@ -32,17 +32,43 @@ struct LogitF16 {
     static __device__ __forceinline__ float value(uint16_t v) { return h2f(v); }
 };
 
-__device__ __forceinline__ double wave_sum(double v) {
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+// The value that a lane gets from another by a data-parallel move, 0 where the move gives none.
+template <int CTRL, int ROWS> __device__ __forceinline__ double moved(double v) {
+    const uint64_t x = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)x, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(x >> 32), CTRL, ROWS, 0xF, false);
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+// Inclusive sums along the lanes: within rows of 16 (shifts by 1, 2, 4, 8), then the ends of rows 0 and 2 into rows 1 and
+// 3, then the end of row 1 into rows 2 and 3.
+__device__ __forceinline__ double wave_scan(double v) {
+    v += moved<0x111, 0xF>(v);
+    v += moved<0x112, 0xF>(v);
+    v += moved<0x114, 0xF>(v);
+    v += moved<0x118, 0xF>(v);
+    v += moved<0x142, 0xA>(v);
+    v += moved<0x143, 0xC>(v);
     return v;
 }
-__device__ __forceinline__ double wave_scan(double v) {     // inclusive
-    for (int d = 1; d < 64; d <<= 1) {
-        const double u = __shfl_up(v, d);
-        if (lane_id() >= d) v += u;
-    }
-    return v;
+__device__ __forceinline__ double lane_value(double v, int lane) {      // lane: the same in all
+    const uint64_t x = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)x, lane), hi = __builtin_amdgcn_readlane((int)(x >> 32), lane);
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
 }
+__device__ __forceinline__ float wave_max(float v) {
+    const int low = __float_as_int(-__builtin_inff());
+#define MOE_MAX_STEP(CTRL, ROWS) \
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(low, __float_as_int(v), CTRL, ROWS, 0xF, false)))
+    MOE_MAX_STEP(0x111, 0xF);
+    MOE_MAX_STEP(0x112, 0xF);
+    MOE_MAX_STEP(0x114, 0xF);
+    MOE_MAX_STEP(0x118, 0xF);
+    MOE_MAX_STEP(0x142, 0xA);
+    MOE_MAX_STEP(0x143, 0xC);
+#undef MOE_MAX_STEP
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ double wave_sum(double v) { return lane_value(wave_scan(v), 63); }
 
 // The sums of max(p - S q, 0) are read by another workgroup of the same launch: written through to memory and read
 // around the caches, as layer_items.h does for smaller types.
@@ -93,10 +119,35 @@ __device__ __forceinline__ Heat heat(const VerifyParams &p, int b) {
     return {1.0 / (double)fminf(T, 3.4028234e38f), !(T > 0.0f)};
 }
 
-// exp((x - top) / T). Equal first: the largest may be infinite; NaN compares false and weighs nothing.
+// e^y for y <= 0 (Cody and Waite's reduction), to about one unit in the last place: y = n log 2 + r with |r| <= log(2) / 2 (log 2 in two parts, the
+// first short enough that n times it is exact), the Taylor polynomial of degree 13 at r (its remainder is below
+// 5e-18), times 2^n. Below e^-800 it is 0 anyway.
+__device__ __forceinline__ double exp_down(double y) {
+    y = fmax(y, -800.0);        // a NaN becomes -800 too
+    const double n = rint(y * 1.4426950408889634);
+    double r = fma(n, -0.6931471803691238, y);          // 0x3FE62E42FEE00000
+    r = fma(n, -1.9082149292705877e-10, r);
+    double e = 1.0 / 6227020800.0;
+    e = fma(e, r, 1.0 / 479001600.0);
+    e = fma(e, r, 1.0 / 39916800.0);
+    e = fma(e, r, 1.0 / 3628800.0);
+    e = fma(e, r, 1.0 / 362880.0);
+    e = fma(e, r, 1.0 / 40320.0);
+    e = fma(e, r, 1.0 / 5040.0);
+    e = fma(e, r, 1.0 / 720.0);
+    e = fma(e, r, 1.0 / 120.0);
+    e = fma(e, r, 1.0 / 24.0);
+    e = fma(e, r, 1.0 / 6.0);
+    e = fma(e, r, 0.5);
+    e = fma(e, r, 1.0);
+    e = fma(e, r, 1.0);
+    return ldexp(e, (int)n);
+}
+
+// exp((x - top) / T), x at most top. Equal first: the largest may be infinite. NaN weighs nothing.
 __device__ __forceinline__ double relative(float x, float top, double inv_t) {
-    const double e = exp(((double)x - (double)top) * inv_t);
-    return x == top ? 1.0 : x < top ? e : 0.0;
+    const double e = exp_down(((double)x - (double)top) * inv_t);
+    return x == top ? 1.0 : e;
 }
 
 // p of index i with logit x in a row whose statistics are r.
@@ -124,7 +175,7 @@ template <typename L> __global__ void __launch_bounds__(256) moe_verify_stats_ke
     float top = -__builtin_inff();
 #pragma unroll
     for (int k = 0; k < SHARE; ++k) top = fmaxf(top, x[k]);      // not a NaN: the other operand
-    for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    top = wave_max(top);
     int best = -1;
     double sum = 0.0;
     if (top > -__builtin_inff()) {
@@ -180,57 +231,65 @@ __device__ int pick_token(const VerifyParams &p, const LogitStat &r, const Heat 
         if (c >= p.chunks) return 0.0;
         return S > 0.0 ? ld_shared64(left + c) : s[c].best < 0 ? 0.0 : s[c].sum * relative(s[c].top, r.top, h.inv) * r.sum;
     };
-    double total = 0.0;
-    for (int c0 = 0; c0 < p.chunks; c0 += 64) total += wave_sum(chunk_weight(c0 + lane));
-    const double goal = (double)u * total;
-    // the chunk: the first whose running sum passes, or (a last rounding) the last with weight
-    int chunk = -1;
-    double run = 0.0, before = 0.0;
-    for (int c0 = 0; c0 < p.chunks; c0 += 64) {
-        const double w = chunk_weight(c0 + lane), cum = run + wave_scan(w);
-        const uint64_t some = __ballot(w > 0.0), past = __ballot(w > 0.0 && cum > goal);
-        if (past || some) {
-            const int l = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some);
-            chunk = c0 + l;
-            before = __shfl(cum - w, l);
-        }
-        if (past) break;
-        run = __shfl(cum, 63);
-    }
+    // Each lane sums a run of neighbouring chunks (at most 16); then the lane, and the chunk of its run, whose running sum
+    // is the first past the goal, or (a last rounding) the last with weight.
+    const int per = (p.chunks + 63) >> 6;
+    double mine = 0.0;
+    for (int k = 0; k < per; ++k) mine += chunk_weight(lane * per + k);
+    const double lanes = wave_scan(mine), goal = (double)u * lane_value(lanes, 63);
+    // the first lane of those with weight whose sum passes; its place and the sum before it
+    auto place = [&](double w, double upto, double *before) {
+        const uint64_t some = __ballot(w > 0.0), over = __ballot(upto > goal) & some;
+        if (!some) return -1;
+        const int l = uniform(over ? __builtin_ctzll(over) : 63 - __builtin_clzll(some));
+        if (l) *before = lane_value(upto, l - 1);
+        return l;
+    };
+    double before = 0.0;
+    int chunk = place(mine, lanes, &before);
     if (chunk < 0) return 0;
+    chunk *= per;
+    if (per > 1) {
+        const double w = lane < per ? chunk_weight(chunk + lane) : 0.0;
+        const int l = place(w, before + wave_scan(w), &before);
+        chunk += max(l, 0);
+    }
     // the same within it
     float x[SHARE], q[SHARE];
     load_share<L>(logits_of<L>(p, row), chunk, p.vocab, -__builtin_inff(), x);
     if (S > 0.0) load_share<LogitF32>(p.draft + (int64_t)row * p.draft_stride, chunk, p.vocab, 0.0f, q);
-    int found = -1;
-    run = before;
+    double w[SHARE], upto[SHARE / 4];
 #pragma unroll
-    for (int k = 0; k < SHARE; k += 4) {
-        double w[4], mine = 0.0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = chunk * VOCAB_CHUNK + share_index(k + e);
-            w[e] = i < p.vocab ? target(r, h, i, x[k + e]) : 0.0;
-            if (S > 0.0) w[e] = fmax(w[e] - S * (double)q[k + e], 0.0);
-            mine += w[e];
-        }
-        const double upto = run + wave_scan(mine);
-        double cum = upto - mine;
-        int first = -1, last = -1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            cum += w[e];
-            if (w[e] > 0.0) last = e;
-            if (w[e] > 0.0 && cum > goal && first < 0) first = e;
-        }
-        const uint64_t past = __ballot(first >= 0), some = __ballot(last >= 0);
-        const int l = past ? __builtin_ctzll(past) : some ? 63 - __builtin_clzll(some) : 0;
-        const int e = __shfl(past ? first : last, l);
-        if (past || some) found = chunk * VOCAB_CHUNK + (k >> 2) * 256 + l * 4 + e;
-        if (past) break;
-        run = __shfl(upto, 63);
+    for (int k = 0; k < SHARE; ++k) {
+        const int i = chunk * VOCAB_CHUNK + share_index(k);
+        w[k] = i < p.vocab ? target(r, h, i, x[k]) : 0.0;
+        if (S > 0.0) w[k] = fmax(w[k] - S * (double)q[k], 0.0);
     }
-    return max(found, 0);
+#pragma unroll
+    for (int k = 0; k < SHARE; k += 4) upto[k / 4] = wave_scan((w[k] + w[k + 1]) + (w[k + 2] + w[k + 3]));
+    int found = 0;
+    bool past = false;
+#pragma unroll
+    for (int k = 0; k < SHARE; k += 4)
+        if (!past) {
+            const double own = (w[k] + w[k + 1]) + (w[k + 2] + w[k + 3]);
+            double run = before + (upto[k / 4] - own);
+            int first = -1, last = -1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                run += w[k + e];
+                if (w[k + e] > 0.0) last = e;
+                if (w[k + e] > 0.0 && run > goal && first < 0) first = e;
+            }
+            const uint64_t over = __ballot(first >= 0), any = __ballot(last >= 0);
+            past = over != 0;
+            if (any) {
+                const int l = past ? __builtin_ctzll(over) : 63 - __builtin_clzll(any);
+                found = chunk * VOCAB_CHUNK + (k >> 2) * 256 + l * 4 + __shfl(past ? first : last, l);
+            }
+            before += lane_value(upto[k / 4], 63);
+        }
+    return found;
 }
 
 // ------------------------------------------------------------------ the walk
@@ -387,8 +446,8 @@ template <typename L> __global__ void __launch_bounds__(1024) moe_verify_walk_ke
     }
 }
 
-// Workgroup (b, y): sums of 16 chunks of sequence b's row, if it waits for them.
-template <typename L> __global__ void __launch_bounds__(1024) moe_verify_left_kernel(VerifyParams p) {
+// Workgroup (b, y): sums of 8 chunks of sequence b's row, if it waits for them.
+template <typename L> __global__ void __launch_bounds__(512) moe_verify_left_kernel(VerifyParams p) {
     __shared__ int ours;
     const int b = (int)blockIdx.x, part = (int)blockIdx.y, lane = lane_id();
     const int wave = uniform((int)threadIdx.x >> 6);
@@ -397,7 +456,7 @@ template <typename L> __global__ void __launch_bounds__(1024) moe_verify_left_ke
     const int first = uniform(p.row_start[b]), n = uniform(p.row_start[b + 1]) - first;     // checked by the walk
     const Heat h = heat(p, b);
     double *left = p.left + (int64_t)b * p.chunks;
-    const int c = part * 16 + wave;
+    const int c = part * 8 + wave;
     if (c < p.chunks) {
         const double s = left_of_chunk<L>(p, p.row_stat[first + st.cur], h, first + st.cur, c, st.S);
         if (lane == 0) st_shared64(left + c, s);
@@ -416,7 +475,7 @@ template <typename L> __global__ void __launch_bounds__(1024) moe_verify_left_ke
         st = p.state[b];
         __syncthreads();
         if (!st.pending) return;
-        for (int k = wave; k < p.chunks; k += 16) {
+        for (int k = wave; k < p.chunks; k += 8) {
             const double s = left_of_chunk<L>(p, p.row_stat[first + st.cur], h, first + st.cur, k, st.S);
             if (lane == 0) st_shared64(left + k, s);
         }
