@@ -41,7 +41,7 @@ struct RopeParams {
 // Workgroups of the attention kernel that a compute unit holds at once: by LDS (two buffers of 64
 // tokens take 512 dim bytes of 160 KB) and by the registers of a wave's queries and sums.
 constexpr int attend_blocks(int dim, int queries) {
-    return dim <= 64 ? (queries == 16 ? 4 : 3) : dim <= 96 ? 3 : dim <= 128 ? 2 : 1;
+    return dim <= 64 ? (queries == 16 ? 4 : queries == 128 ? 2 : 3) : dim <= 96 ? 3 : dim <= 128 ? 2 : 1;
 }
 
 constexpr int ATTEND_MOST_RANGES = 1024;
