@@ -119,6 +119,12 @@ template <int MQ> __device__ __forceinline__ SeqWork seq_work(const AttendParams
     return w;
 }
 
+// a / b, neither negative: in 32 bits where both fit (a 64-bit division takes some 150 instructions, and a short
+// call has five of them in a row before its first load).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 struct PlanLds {
     int64_t wave[4];
     int64_t base;
@@ -159,8 +165,8 @@ __device__ __forceinline__ bool find_range(const AttendParams &p, PlanLds &s, in
     *total = N;
     *groups = G;
     if (at >= G) return false;
-    *x = at * N / G;
-    *xe = (at + 1) * N / G;
+    *x = divide(at * N, G);
+    *xe = divide((at + 1) * N, G);
     if (sum && before <= *x && *x < before + sum) {
         int q = tid * per;
         for (int64_t t; *x >= before + (t = seq_work<MQ>(p, q, false).units); ++q) before += t;
@@ -215,11 +221,11 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
         }
         const int first = uniform(sq.first), n = uniform(sq.n), len = uniform(sq.len), end = uniform(sq.end);
         const int tts = uniform(sq.tts), mts = uniform(sq.mts), all_units = tts + ITEM_COST;
-        const int64_t rel = x - base, item = rel / all_units;
+        const int64_t rel = x - base, item = divide(rel, all_units);
         const int u_from = uniform((int)(rel - item * all_units));
         const int u_to = uniform((int)min((int64_t)all_units, u_from + (xe - x)));
         const int t_from = max(0, u_from - ITEM_COST), t_to = u_to - ITEM_COST;
-        const int mt = uniform((int)(item % mts)), h = uniform((int)(item / mts));
+        const int h = uniform((int)divide(item, mts)), mt = uniform((int)(item - (int64_t)h * mts));
         x += u_to - u_from;
         if (t_to <= t_from) continue;
         const int queries = min((int64_t)MQ, (int64_t)n * p.group - (int64_t)mt * MQ);
@@ -484,7 +490,7 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
             part.mt = mt;
             part.head = h;
             part.queries = queries;
-            part.count = (int)((last * groups - 1) / total) - w + 1;
+            part.count = (int)divide(last * groups - 1, total) - w + 1;
         }
         __syncthreads();
     }
