@@ -169,7 +169,7 @@ __device__ __forceinline__ bool find_range(const AttendParams &p, PlanLds &s, in
     *xe = divide((at + 1) * N, G);
     if (sum && before <= *x && *x < before + sum) {
         int q = tid * per;
-        for (int64_t t; *x >= before + (t = seq_work<MQ>(p, q, false).units); ++q) before += t;
+        for (int64_t t; q + 1 < p.c.seqs && *x >= before + (t = seq_work<MQ>(p, q, false).units); ++q) before += t;
         s.b = q;
         s.base = before;
     }
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
         SeqWork sq = seq_work<MQ>(p, b, false);
         if (x >= base + sq.units) {
             base += sq.units;
-            ++b;
+            if (++b >= p.c.seqs) break;     // cannot be, unless lengths change while this runs
             continue;
         }
         const int first = uniform(sq.first), n = uniform(sq.n), len = uniform(sq.len), end = uniform(sq.end);
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
             part.mt = mt;
             part.head = h;
             part.queries = queries;
-            part.count = (int)divide(last * groups - 1, total) - w + 1;
+            part.count = (int)min(divide(last * groups - 1, total), groups - 1) - w + 1;
         }
         __syncthreads();
     }

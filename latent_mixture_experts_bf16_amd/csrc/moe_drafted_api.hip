@@ -375,7 +375,10 @@ extern "C" int moe_tree_attend(const moe_paged_cache *c, int32_t rows, const voi
     else
         attend_kernels<false>(p.c.dim, shape.queries, &main, &join);
     if ((rc = launch("tree_attend", main, dim3((unsigned)shape.ranges), dim3(256), p, hip_stream))) return rc;
-    return launch("tree_attend join", join, dim3(512), dim3(256), p, hip_stream);
+    // More workgroups join more queries at once, but each lists the work first: few queries a key head make few
+    // (item, query) pairs (one row over 777 tokens: 5.9 us with 512, 6.4 with 1024), many make thousands (64-row trees
+    // over 4100: 14.7 and 10.3).
+    return launch("tree_attend join", join, dim3(shape.queries == 16 ? 512 : 1024), dim3(256), p, hip_stream);
 }
 
 // ------------------------------------------------------------------ draft verification
@@ -430,7 +433,7 @@ template <typename L> static int verify_launches(VerifyParams &p, void *stream) 
     for (int i = 0; i < rounds; ++i) {
         p.last_round = i == rounds - 1;
         if ((rc = launch("draft_verify left", moe_verify_left_kernel<L>,
-                         dim3((unsigned)p.seqs, (unsigned)(p.chunks + 7) / 8), dim3(512), p, stream)))
+                         dim3((unsigned)p.seqs, (unsigned)(p.chunks + 3) / 4), dim3(256), p, stream)))
             return rc;
     }
     return MOE_OK;

@@ -223,19 +223,20 @@ template <typename L> __global__ void __launch_bounds__(256) moe_verify_stats_ke
 
 // ------------------------------------------------------------------ picking
 
-// Statistics of a whole row from its chunks, the same in every lane.
+// Statistics of a whole row from its chunks, the same in every lane. Each lane has a run of neighbouring chunks (at most
+// 16), so that the lowest index is that of the first lane with the largest logit.
 __device__ __forceinline__ LogitStat join_chunks(const VerifyParams &p, const Heat &h, int row) {
     const LogitStat *s = p.chunk_stat + (int64_t)row * p.chunks;
+    const int per = (p.chunks + 63) >> 6, from = lane_id() * per, to = min(p.chunks, from + per);
     LogitStat r = {0.0, -__builtin_inff(), -1};
-    for (int c = lane_id(); c < p.chunks; c += 64)
+    for (int c = from; c < to; ++c)
         if (s[c].top > r.top) { r.top = s[c].top; r.best = s[c].best; }
-    for (int d = 32; d; d >>= 1) {
-        const float t = __shfl_xor(r.top, d);
-        const int i = __shfl_xor(r.best, d);
-        if (i >= 0 && (t > r.top || (t == r.top && i < r.best))) { r.top = t; r.best = i; }
-    }
+    const float top = wave_max(r.top);
+    const uint64_t have = __ballot(r.top == top && r.best >= 0);
+    r.top = top;
+    r.best = have ? __builtin_amdgcn_readlane(r.best, (int)__builtin_ctzll(have)) : -1;
     if (r.best < 0 || h.greedy) return r;
-    for (int c = lane_id(); c < p.chunks; c += 64) r.sum += s[c].sum * relative(s[c].top, r.top, h.inv);
+    for (int c = from; c < to; ++c) r.sum += s[c].sum * relative(s[c].top, r.top, h.inv);
     r.sum = 1.0 / wave_sum(r.sum);
     return r;
 }
@@ -472,8 +473,8 @@ template <typename L> __global__ void __launch_bounds__(1024) moe_verify_walk_ke
     }
 }
 
-// Workgroup (b, y): sums of 8 chunks of sequence b's row, if it waits for them.
-template <typename L> __global__ void __launch_bounds__(512) moe_verify_left_kernel(VerifyParams p) {
+// Workgroup (b, y): sums of 4 chunks of sequence b's row, if it waits for them.
+template <typename L> __global__ void __launch_bounds__(256, 4) moe_verify_left_kernel(VerifyParams p) {
     __shared__ int ours;
     const int b = (int)blockIdx.x, part = (int)blockIdx.y, lane = lane_id();
     const int wave = uniform((int)threadIdx.x >> 6);
@@ -482,7 +483,7 @@ template <typename L> __global__ void __launch_bounds__(512) moe_verify_left_ker
     const int first = uniform(p.row_start[b]), n = uniform(p.row_start[b + 1]) - first;     // checked by the walk
     const Heat h = heat(p, b);
     double *left = p.left + (int64_t)b * p.chunks;
-    const int c = part * 8 + wave;
+    const int c = part * 4 + wave;
     if (c < p.chunks) {
         const double s = left_of_chunk<L>(p, p.row_stat[first + st.cur], h, first + st.cur, c, st.S);
         if (lane == 0) st_shared64(left + c, s);
@@ -501,7 +502,7 @@ template <typename L> __global__ void __launch_bounds__(512) moe_verify_left_ker
         st = p.state[b];
         __syncthreads();
         if (!st.pending) return;
-        for (int k = wave; k < p.chunks; k += 8) {
+        for (int k = wave; k < p.chunks; k += 4) {
             const double s = left_of_chunk<L>(p, p.row_stat[first + st.cur], h, first + st.cur, k, st.S);
             if (lane == 0) st_shared64(left + k, s);
         }
