@@ -71,12 +71,12 @@ struct AttendParams {
 constexpr int MAX_VOCAB = 1 << 20;
 constexpr int VOCAB_CHUNK = 1024;   // logits of a row that one wave takes at a time
 
-// Of one chunk of a row, and of a whole row: the largest logit, its lowest index, and the sum of
-// exp((z - top) / T) (chunk) or 1 / that sum (row).
+// Of one chunk of a row, and of a whole row: the largest logit; where T <= 0 its lowest index, else
+// the sum of exp((z - top) / T) (chunk) or 1 / that sum (row).
 struct LogitStat {
     double sum;
     float top;
-    int32_t best;               // -1: nothing above -infinity
+    int32_t best;               // -1: nothing above -infinity; where T > 0 no more than that there is something
 };
 
 // Where the walk of one sequence stands between launches.

@@ -119,37 +119,46 @@ __device__ __forceinline__ Heat heat(const VerifyParams &p, int b) {
     return {1.0 / (double)fminf(T, 3.4028234e38f), !(T > 0.0f)};
 }
 
-// e^y for y <= 0, to about one unit in the last place: y = n log 2 + r with |r| <= log(2) / 2 (Cody and Waite's reduction:
-// log 2 in two parts, the first short enough that n times it is exact), the Taylor polynomial of degree 12 at r (its
-// remainder is below 2e-16), times 2^n. n is rounded by adding 1.5 2^52, which leaves it in the low bits, and
-// added to the exponent: conversions and scalings of 64-bit numbers run at a quarter of the rate of sums and products.
-// Below e^-708, and for a NaN, 0.
+// e^y for y <= 0, to about one unit in the last place: y = n log(2) / 32 + r with |r| <= log(2) / 64 (Cody and Waite's
+// reduction: the constant in two parts, the first short enough that n times it is exact), then 2^(n / 32) from a table of
+// 32 (they lie on different banks of LDS) and the exponent, times the Taylor polynomial of degree 6 at r (its remainder
+// is below 4e-18). n is rounded by adding 1.5 2^52, which leaves it in the low bits. Below e^-708, and for a NaN, 0.
 //
-// The coefficients stay in scalar registers: left to itself the compiler moves each of them into the vector registers that
-// the sum goes to, two moves a product (40 -> 37 us over 64 x 5 rows of 100003).
-__device__ __forceinline__ double fma_scalar(double a, double b, double c) {
-    double d;
-    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
-    return d;
+// Without the table, at degree 12, the statistics of 64 x 5 rows of 100003 took 37 us, with it 36; the library's
+// function 41.
+__device__ const double EXP2_TABLE[32] = {
+    1.0, 1.0218971486541166, 1.0442737824274138, 1.0671404006768237,
+    1.0905077326652577, 1.1143867425958924, 1.1387886347566916, 1.1637248587775775,
+    1.189207115002721, 1.215247359980469, 1.241857812073484, 1.2690509571917332,
+    1.2968395546510096, 1.3252366431597413, 1.3542555469368927, 1.383909881963832,
+    1.4142135623730951, 1.4451808069770467, 1.4768261459394993, 1.5091644275934228,
+    1.5422108254079407, 1.5759808451078865, 1.6104903319492543, 1.645755478153965,
+    1.681792830507429, 1.718619298122478, 1.7562521603732995, 1.7947090750031072,
+    1.8340080864093424, 1.8741676341103, 1.9152065613971474, 1.9571441241754002,
+};
+__device__ __forceinline__ double *exp_table() {
+    __shared__ double t[32];
+    return t;
+}
+// Every kernel below calls this first, with all its threads.
+__device__ __forceinline__ void fill_exp_table() {
+    if (threadIdx.x < 32) exp_table()[threadIdx.x] = EXP2_TABLE[threadIdx.x];
+    __syncthreads();
 }
 __device__ __forceinline__ double exp_down(double y) {
     constexpr double ROUND = 6755399441055744.0;
-    const double t = fma(y, 1.4426950408889634, ROUND), n = t - ROUND;
-    double r = fma(n, -0.6931471803691238, y);          // 0x3FE62E42FEE00000
-    r = fma(n, -1.9082149292705877e-10, r);
-    double e = fma_scalar(r, 1.0 / 479001600.0, 1.0 / 39916800.0);
-    e = fma_scalar(e, r, 1.0 / 3628800.0);
-    e = fma_scalar(e, r, 1.0 / 362880.0);
-    e = fma_scalar(e, r, 1.0 / 40320.0);
-    e = fma_scalar(e, r, 1.0 / 5040.0);
-    e = fma_scalar(e, r, 1.0 / 720.0);
-    e = fma_scalar(e, r, 1.0 / 120.0);
-    e = fma_scalar(e, r, 1.0 / 24.0);
-    e = fma_scalar(e, r, 1.0 / 6.0);
+    const double t = fma(y, 46.16624130844683, ROUND), n = t - ROUND;
+    double r = fma(n, -0.02166084938653512, y);
+    r = fma(n, -5.9631716539705866e-12, r);
+    const int k = (int)(uint32_t)(uint64_t)__double_as_longlong(t);
+    const double m = exp_table()[k & 31];
+    double e = fma(r, 1.0 / 720.0, 1.0 / 120.0);
+    e = fma(e, r, 1.0 / 24.0);
+    e = fma(e, r, 1.0 / 6.0);
     e = fma(e, r, 0.5);
     e = fma(e, r, 1.0);
-    e = fma(e, r, 1.0);
-    const uint64_t bits = (uint64_t)__double_as_longlong(e) + ((uint64_t)__double_as_longlong(t) << 52);
+    e = fma(m, e * r, m);
+    const uint64_t bits = (uint64_t)__double_as_longlong(e) + ((uint64_t)(uint32_t)((k >> 5) * (1 << 20)) << 32);
     return y >= -708.0 ? __longlong_as_double((long long)bits) : 0.0;
 }
 
@@ -173,7 +182,7 @@ template <typename L> __device__ __forceinline__ const typename L::T *logits_of(
 
 // ------------------------------------------------------------------ stats
 
-// Largest logit, its lowest index and the sum of chunk c, in registers.
+// Largest logit of chunk c, in registers, and what the temperature asks for: its lowest index, or the sum.
 __device__ __forceinline__ LogitStat chunk_stat(const Heat &h, int c, const float *x) {
     float top = -__builtin_inff();
 #pragma unroll
@@ -181,19 +190,22 @@ __device__ __forceinline__ LogitStat chunk_stat(const Heat &h, int c, const floa
     top = wave_max(top);
     LogitStat r = {0.0, top, -1};
     if (!(top > -__builtin_inff())) return r;
-    // the lowest index: the first quarter of the chunk that has the value, its first lane, that lane's first
+    r.best = c * VOCAB_CHUNK;
+    if (h.greedy) {
+        // the first quarter of the chunk that has the value, its first lane, that lane's first
 #pragma unroll
-    for (int k = SHARE - 4; k >= 0; k -= 4) {
-        int at = 4;
+        for (int k = SHARE - 4; k >= 0; k -= 4) {
+            int at = 4;
 #pragma unroll
-        for (int e = 3; e >= 0; --e) at = x[k + e] == top ? e : at;
-        const uint64_t some = __ballot(at < 4);
-        if (some) {
-            const int l = __builtin_ctzll(some);
-            r.best = c * VOCAB_CHUNK + (k >> 2) * 256 + l * 4 + __builtin_amdgcn_readlane(at, l);
+            for (int e = 3; e >= 0; --e) at = x[k + e] == top ? e : at;
+            const uint64_t some = __ballot(at < 4);
+            if (some) {
+                const int l = __builtin_ctzll(some);
+                r.best = c * VOCAB_CHUNK + (k >> 2) * 256 + l * 4 + __builtin_amdgcn_readlane(at, l);
+            }
         }
+        return r;
     }
-    if (h.greedy) return r;
     double sum = 0.0;
     if (top == __builtin_inff())
 #pragma unroll
@@ -206,13 +218,16 @@ __device__ __forceinline__ LogitStat chunk_stat(const Heat &h, int c, const floa
 }
 
 // One chunk a wave: two, with the row's sequence looked up once, took 40 us instead of 37 over 64 x 5 rows of 100003.
-// What bounds it is the 64-bit arithmetic, some 24 operations an element (117 MB at 3.2 TB/s; a copy moves 4.8).
+// What bounds it is the vector instructions, some 20 of 64 bits an element (117 MB in 36 us, 3.3 TB/s; a copy moves
+// 4.8): leaving out the search for the largest logit's index where T > 0 changed nothing that could be measured.
 template <typename L> __global__ void __launch_bounds__(256) moe_verify_stats_kernel(VerifyParams p) {
     const int row = (int)(blockIdx.z * gridDim.y + blockIdx.y), lane = lane_id();
     const int c = (int)blockIdx.x * 4 + uniform((int)threadIdx.x >> 6);
-    if (row >= p.rows || c >= p.chunks) return;
-    float x[SHARE];      // on its way before the row's sequence is looked up
-    load_share<L>(logits_of<L>(p, row), c, p.vocab, -__builtin_inff(), x);
+    const bool some = row < p.rows && c < p.chunks;
+    float x[SHARE];      // on its way before the table is filled and the row's sequence looked up
+    if (some) load_share<L>(logits_of<L>(p, row), c, p.vocab, -__builtin_inff(), x);
+    fill_exp_table();
+    if (!some) return;
     int first = 0;
     // a row of no sequence is not walked; but where row_start is not ascending the walk may read it all the same
     const int b = seq_of_row(p.row_start, p.seqs, row, &first);
@@ -444,6 +459,7 @@ __device__ bool walk(const VerifyParams &p, const Heat &h, int b, int first, int
 // logits, 16 us for 8 trees of up to 16 rows (each row's pick, 16 at once), 15 us for 64 chains of 6.
 template <typename L> __global__ void __launch_bounds__(1024) moe_verify_walk_kernel(VerifyParams p) {
     const int b = (int)blockIdx.x, tid = (int)threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
+    fill_exp_table();
     int first = 0;
     const int n = seq_rows(p.row_start, b, p.rows, &first, p.flags);
     WalkState &out = p.state[b];
@@ -484,7 +500,8 @@ template <typename L> __global__ void __launch_bounds__(256, 4) moe_verify_left_
     const int b = (int)blockIdx.x, part = (int)blockIdx.y, lane = lane_id();
     const int wave = uniform((int)threadIdx.x >> 6);
     WalkState st = p.state[b];
-    if (!st.pending) return;
+    if (!st.pending) return;       // all threads of the workgroup, or none
+    fill_exp_table();
     const int first = uniform(p.row_start[b]), n = uniform(p.row_start[b + 1]) - first;     // checked by the walk
     const Heat h = heat(p, b);
     double *left = p.left + (int64_t)b * p.chunks;
