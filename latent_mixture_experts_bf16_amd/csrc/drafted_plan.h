@@ -84,8 +84,6 @@ struct WalkState {
     double S, rest;             // as moe_drafted.h names them
     int32_t cur, kept, after;   // the row, the rows of the path so far, the last child that was tested
     int32_t pending;            // 1: waits for the sum of max(p - S q, 0) over row cur
-    uint32_t done;              // workgroups that have added their part of it
-    uint32_t pad;
 };
 
 struct VerifyParams {
@@ -104,6 +102,8 @@ struct VerifyParams {
     int32_t *pick;              // [rows]: without draft_probs, the token drawn after the row
     double *left;               // [seqs][chunks]: sums of max(p - S q, 0)
     WalkState *state;           // [seqs]
+    uint32_t *arrived;          // [seqs]: workgroups that have added their part of a sum; apart from the state, which is
+                                // copied and stored whole
 };
 
 struct KeepParams {

@@ -400,6 +400,7 @@ static int64_t verify_layout(int64_t rows, int64_t seqs, int64_t vocab, char *ba
     const int64_t left = state + seqs * (int64_t)sizeof(WalkState);
     const int64_t token_p = left + seqs * chunks * 8;
     const int64_t pick = token_p + rows * 8;
+    const int64_t arrived = pick + rows * 4;
     if (p) {
         p->chunks = (int32_t)chunks;
         p->chunk_stat = (LogitStat *)base;
@@ -408,8 +409,9 @@ static int64_t verify_layout(int64_t rows, int64_t seqs, int64_t vocab, char *ba
         p->left = (double *)(base + left);
         p->token_p = (double *)(base + token_p);
         p->pick = (int32_t *)(base + pick);
+        p->arrived = (uint32_t *)(base + arrived);
     }
-    return pick + rows * 4;
+    return arrived + seqs * 4;
 }
 
 extern "C" int64_t moe_draft_verify_workspace(int32_t rows, int32_t seqs, int32_t vocab) {

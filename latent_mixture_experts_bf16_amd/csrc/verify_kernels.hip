@@ -463,6 +463,7 @@ template <typename L> __global__ void __launch_bounds__(1024) moe_verify_walk_ke
     int first = 0;
     const int n = seq_rows(p.row_start, b, p.rows, &first, p.flags);
     WalkState &out = p.state[b];
+    if (tid == 0) p.arrived[b] = 0;
     if (n == 0) {
         if (tid == 0) {
             p.n_keep[b] = 0;
@@ -485,7 +486,7 @@ template <typename L> __global__ void __launch_bounds__(1024) moe_verify_walk_ke
     }
     __syncthreads();
     if (wave == 0) {
-        WalkState st = {0.0, 1.0, 0, 1, 0, 0, 0, 0};
+        WalkState st = {0.0, 1.0, 0, 1, 0, 0};
         st.pending = !walk<L>(p, h, b, first, n, st);
         if (lane == 0) out = st;
     }
@@ -510,7 +511,7 @@ template <typename L> __global__ void __launch_bounds__(256, 4) moe_verify_left_
         const double v = left_of_chunk<L>(p, p.row_stat[first + st.cur], h, first + st.cur, c, st.S);
         if (lane == 0) st_shared64(left + c, v);
     }
-    if (!last_arriver(&p.state[b].done, gridDim.y, &ours)) return;
+    if (!last_arriver(p.arrived + b, gridDim.y, &ours)) return;
     for (;;) {
         if (wave == 0) {
             double sum = 0.0;

@@ -185,3 +185,24 @@ def test_rope_rows_of_many_sequences():
     pages = [P.place(b, lens[b]) for b in range(5000) if rows[b]]
     pg, sl = torch.tensor([p for p, _ in pages]), torch.tensor([s for _, s in pages])
     assert torch.equal(P.k[pg, sl].view(R, 32), x) and torch.equal(P.v[pg, sl].view(R, 32), x)
+
+
+@pytest.mark.parametrize("seqs,V", [(64, 131072), (300, 16385)])
+def test_verify_refusals_of_a_full_batch(seqs, V):
+    """Sampled trees whose siblings are refused one after another, over more chunks than the card's workgroups hold at
+    once (seqs * V / 4096 of 1024): a workgroup that starts late finds others' arrivals counted, in every launch. The
+    drafts are drawn apart from the target, so most sequences refuse two siblings or more at one row."""
+    parent = [-1, 0, 0, 0, 0, 1]
+    n, R = len(parent), len(parent) * seqs
+    g = torch.Generator(device="cuda")
+    g.manual_seed(V)
+    z = torch.empty((R, V), device="cuda").normal_(0, 3, generator=g)
+    q = torch.softmax(torch.empty((R, V), device="cuda").normal_(0, 3, generator=g), 1)
+    at = torch.tensor([b * n + max(p, 0) for b in range(seqs) for p in parent], device="cuda")
+    tokens = torch.multinomial(q[at], 1, generator=g)[:, 0].tolist()
+    r = np.random.default_rng(seqs)
+    T = (0.7 + 0.1 * (np.arange(seqs) % 5)).tolist()
+    for _ in range(2):
+        ut, up = r.random(R).astype(np.float32), r.random(R).astype(np.float32)
+        got = _verify_check(z, tokens, [n] * seqs, [parent] * seqs, ut, up, q, T)
+        assert (got[0] == 1).sum() > seqs // 2      # all four siblings refused
