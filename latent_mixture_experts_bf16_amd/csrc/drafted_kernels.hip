@@ -132,57 +132,76 @@ ROPE_KERNELS(true);
 
 // ------------------------------------------------------------------ path keeping
 
-// One workgroup per sequence. Row i of the path comes from a row at or after i (paths ascend), so
-// with each thread owning the same 16 bytes of every row, and loading KEEP_STEP rows before it
-// stores them, nothing is overwritten before it is read: every source of a later step lies
-// after the places of the earlier ones. 64 paths of up to 24 rows: 8 us, a launch and three loads one after another
-// (path, page, rows), twice; one path: 5 us. 16 rows a step took as long.
-constexpr int KEEP_STEP = 8;
+// One workgroup per sequence. The path is checked, and the slots that its rows come from and go to are looked up, before
+// the first one moves: a path out of order, or a page that the cache does not have, moves nothing. Row i of the path comes
+// from a row at or after i (paths ascend), so with each thread owning the same 16 bytes of every row, and loading KEEP_STEP
+// rows before it stores them, nothing is overwritten before it is read: every source of a later step lies after the
+// places of the earlier ones. Bound by a launch and three loads one after another (path, page, rows): 64 paths of up to
+// 24 rows take 5.5 us as a pass among others (7.2 where every thread looks the slots up for itself at each step), one 5.3.
+constexpr int KEEP_STEP = 8, KEEP_CHUNK = 256;
 
-__global__ void __launch_bounds__(256) moe_keep_kernel(KeepParams p) {
+__global__ void __launch_bounds__(KEEP_CHUNK) moe_keep_kernel(KeepParams p) {
+    __shared__ int4 moves[KEEP_CHUNK];    // of a chunk of the path: page and slot from, page and slot to; page -1: it stays
     const int b = (int)blockIdx.x, tid = (int)threadIdx.x;
     int first = 0;
     const int n = seq_rows(p.row_start, b, p.rows, &first, p.c.flags);
     const int len = p.c.len[b], keep = p.n_keep[b];
     const int32_t *path = p.path + first;
-    bool bad = keep < 0 || keep > n;
-    for (int i = tid; !bad && i < keep; i += 256) {
+    auto look_up = [&](int i) {
+        int4 m = make_int4(-1, 0, 0, 0);
+        const int s = path[i];
+        const bool ok = s == i || (find_slot(p.c, b, (int64_t)len + s, &m.x, &m.y) &&
+                                   find_slot(p.c, b, (int64_t)len + i, &m.z, &m.w));
+        moves[tid] = m;
+        return ok;
+    };
+    const bool bad_len = len < 0 || (int64_t)len + keep > p.c.cap;
+    bool bad_path = keep < 0 || keep > n, bad_page = false;
+    // the first chunk last, whose slots are then in LDS
+    for (int i = bad_path ? -1 : ((keep - 1) & ~(KEEP_CHUNK - 1)) + tid; i >= 0; i -= KEEP_CHUNK) {
+        if (i >= keep) continue;
         const int s = path[i], prev = i ? path[i - 1] : -1;
-        bad = s <= prev || s >= n;
+        if (s <= prev || s >= n) bad_path = true;
+        else if (!bad_len && !look_up(i)) bad_page = true;
     }
-    bad = __syncthreads_or(bad) != 0;
-    if (bad || len < 0 || (int64_t)len + keep > p.c.cap) {
+    if (bad_path) raise_flag(p.c.flags, MOE_FLAG_PATH);
+    const bool bad = __syncthreads_or(bad_path || bad_page) != 0;
+    if (bad || bad_len) {
         if (tid == 0) {
-            raise_flag(p.c.flags, bad ? MOE_FLAG_PATH : MOE_FLAG_LEN);
+            if (!bad) raise_flag(p.c.flags, MOE_FLAG_LEN);
             p.new_len[b] = len;
         }
         return;
     }
     const int per = p.c.dim / 8, heads = p.c.heads;
-    for (int u = tid; u < 2 * heads * per; u += 256) {
-        const bool value = u >= heads * per;
-        const int w = value ? u - heads * per : u;
-        const int h = w / per, d = (w - h * per) * 8;
-        const KvView &kv = value ? p.c.v : p.c.k;
-        uint16_t *base = (uint16_t *)kv.p + h * kv.head + d;
-        for (int i0 = 0; i0 < keep; i0 += KEEP_STEP) {
-            uint4 x[KEEP_STEP];
-            int64_t to[KEEP_STEP];
+    for (int c0 = 0; c0 < keep; c0 += KEEP_CHUNK) {
+        const int here = min(KEEP_CHUNK, keep - c0);
+        if (c0) {
+            __syncthreads();
+            if (tid < here) look_up(c0 + tid);
+            __syncthreads();
+        }
+        for (int u = tid; u < 2 * heads * per; u += KEEP_CHUNK) {
+            const bool value = u >= heads * per;
+            const int w = value ? u - heads * per : u;
+            const int h = w / per, d = (w - h * per) * 8;
+            const KvView &kv = value ? p.c.v : p.c.k;
+            uint16_t *base = (uint16_t *)kv.p + h * kv.head + d;
+            for (int i0 = 0; i0 < here; i0 += KEEP_STEP) {
+                uint4 x[KEEP_STEP];
+                int64_t to[KEEP_STEP];
 #pragma unroll
-            for (int k = 0; k < KEEP_STEP; ++k) {
-                to[k] = -1;
-                const int i = i0 + k;
-                if (i >= keep || path[i] == i) continue;
-                int ps, ss, pd, sd;
-                if (!find_slot(p.c, b, (int64_t)len + path[i], &ps, &ss) ||
-                    !find_slot(p.c, b, (int64_t)len + i, &pd, &sd))
-                    continue;
-                x[k] = *(const uint4 *)(base + ps * kv.page + ss * kv.slot);
-                to[k] = pd * kv.page + sd * kv.slot;
+                for (int k = 0; k < KEEP_STEP; ++k) {
+                    const int4 m = moves[min(i0 + k, here - 1)];
+                    to[k] = -1;
+                    if (i0 + k >= here || m.x < 0) continue;
+                    x[k] = *(const uint4 *)(base + m.x * kv.page + m.y * kv.slot);
+                    to[k] = m.z * kv.page + m.w * kv.slot;
+                }
+#pragma unroll
+                for (int k = 0; k < KEEP_STEP; ++k)
+                    if (to[k] >= 0) *(uint4 *)(base + to[k]) = x[k];
             }
-#pragma unroll
-            for (int k = 0; k < KEEP_STEP; ++k)
-                if (to[k] >= 0) *(uint4 *)(base + to[k]) = x[k];
         }
     }
     // every thread read the length before the barrier above, so the cache's own may be written

@@ -653,3 +653,46 @@ def test_the_operators_in_a_graph():
         assert all(torch.equal(a, b) for a, b in zip(b1, b2)), s
         assert torch.equal(P.k, P2.k) and torch.equal(P.v, P2.v)
     P.cache.status(), v.status()
+
+
+@pytest.mark.parametrize("rows", [[20, 5], [700, 5]])
+def test_keep_with_a_bad_page_moves_nothing(rows):
+    """A page that the cache does not have, at a source or a place of the path, early or late in it: the whole path stays
+    where it was and the length too; the other sequence's path is kept."""
+    lens = [20, 33]
+    path = [0] + list(range(2, rows[0])) + [-1] + [0, 2, 4, -1, -1]
+    keep = [rows[0] - 1, 3]
+    P = Paged(lens, rows, 2, 64, 16, torch.bfloat16, seed=3)
+    starts, n_keep, path_dev, new = _i32(_starts(rows)), _i32(keep), _i32(path), _i32([0, 0])
+    k0, v0, table = P.k.clone(), P.v.clone(), P.table.clone()
+    wk, wv = k0.clone(), v0.clone()
+    for i, s in enumerate((0, 2, 4)):
+        wk[P.place(1, 33 + i)], wv[P.place(1, 33 + i)] = k0[P.place(1, 33 + s)], v0[P.place(1, 33 + s)]
+    last = (lens[0] + rows[0] - 1) // 16      # the page of the last source
+    for entry in (lens[0] // 16, last):       # that of the first place, too
+        for bad in (-1, P.k.shape[0], 1 << 30):
+            P.table[0, entry] = bad
+            P.cache.keep(starts, n_keep, path_dev, new_len=new)
+            P.table.copy_(table)
+            with pytest.raises(B.MoeError, match="page") as e:
+                P.cache.status()
+            assert "path" not in str(e.value)
+            assert torch.equal(P.k, wk) and torch.equal(P.v, wv) and new.tolist() == [20, 36], (entry, bad)
+            P.k.copy_(k0), P.v.copy_(v0)
+
+
+def test_keep_long_paths():
+    """Paths of more rows than a workgroup has threads, bit for bit."""
+    lens, rows = [5, 100], [900, 513]
+    P = Paged(lens, rows, 1, 64, 48, torch.float16, seed=4)
+    r = np.random.default_rng(3)
+    kept = [[0] + sorted(r.choice(np.arange(1, n), n * 2 // 3, replace=False).tolist()) for n in rows]
+    wk, wv = P.k.clone(), P.v.clone()
+    for b, t in enumerate(lens):
+        for i, s in enumerate(kept[b]):
+            wk[P.place(b, t + i)], wv[P.place(b, t + i)] = P.k[P.place(b, t + s)], P.v[P.place(b, t + s)]
+    path = [x for k, n in zip(kept, rows) for x in k + [-1] * (n - len(k))]
+    got = P.cache.keep(_i32(_starts(rows)), _i32([len(k) for k in kept]), _i32(path))
+    P.cache.status()
+    assert got.tolist() == [t + len(k) for t, k in zip(lens, kept)]
+    assert torch.equal(P.k, wk) and torch.equal(P.v, wv)
