@@ -43,7 +43,9 @@ __global__ void __launch_bounds__(256) moe_rope_kernel(RopeParams p) {
         if (tid == 0) raise_flag(p.c.flags, MOE_FLAG_ROWS);
         return;
     }
-    const int64_t token = (int64_t)p.c.len[b] + (row - first);
+    const int len = p.c.len[b];
+    const bool len_ok = len >= 0 && len <= p.c.cap;
+    const int64_t token = (int64_t)len + (row - first);
     if (tid < p.pairs) {
         const int64_t pos = p.positions ? (int64_t)p.positions[row] : token;
         const double turns = (double)pos * p.freqs[tid] * 0.15915494309189533577;   // 1 / (2 pi)
@@ -51,14 +53,14 @@ __global__ void __launch_bounds__(256) moe_rope_kernel(RopeParams p) {
         cs[tid] = make_float2(cospif(t) * p.magnitude, sinpif(t) * p.magnitude);
     }
     int page = 0, slot = 0;
-    bool ok = token >= 0 && token < p.c.cap;
+    bool ok = len_ok && token < p.c.cap;     // a row after a negative length would fall on a cached token
     if (ok) {
         const int at = (int)token / p.c.page;
         page = p.c.table[b * p.c.table_stride + at];
         slot = (int)token - at * p.c.page;
         ok = page >= 0 && page < p.c.pages;
     }
-    if (!ok && tid == 0) raise_flag(p.c.flags, MOE_FLAG_PAGE);
+    if (!ok && tid == 0) raise_flag(p.c.flags, len_ok ? MOE_FLAG_PAGE : MOE_FLAG_LEN);
     __syncthreads();
 
     const int D = p.c.dim, rd = 2 * p.pairs;

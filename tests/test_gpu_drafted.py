@@ -696,3 +696,24 @@ def test_keep_long_paths():
     P.cache.status()
     assert got.tolist() == [t + len(k) for t, k in zip(lens, kept)]
     assert torch.equal(P.k, wk) and torch.equal(P.v, wv)
+
+
+def test_append_with_a_bad_length_writes_nothing():
+    """Rows of a sequence whose length is negative or past the table: token len + i of a later row may be a cached one.
+    Its keys and values stay as they were, the other sequence's are appended, the queries are rotated all the same."""
+    P = Paged([40, 20], [5, 2], 1, 64, 16, torch.bfloat16, seed=3)
+    rope, starts = D.Rope(D.rope_frequencies(64)[0]), _i32([0, 5, 7])
+    q = torch.randn((7, 64), generator=_gen(1)).to(torch.bfloat16).cuda()
+    pos = _i32([40, 41, 42, 43, 44, 20, 21])
+    k0, v0 = P.k.clone(), P.v.clone()
+    want = P.cache.append(rope, q, q, q, starts, positions=pos)
+    P.cache.status()
+    wk, wv = k0.clone(), v0.clone()
+    for t in (20, 21):
+        wk[P.place(1, t)], wv[P.place(1, t)] = P.k[P.place(1, t)], P.v[P.place(1, t)]
+    for bad in (-1, -3, -2 ** 31, P.table.shape[1] * 16 + 1, 2 ** 31 - 1):
+        P.k.copy_(k0), P.v.copy_(v0), P.len.copy_(_i32([bad, 20]))
+        got = P.cache.append(rope, q, q, q, starts, positions=pos)
+        with pytest.raises(B.MoeError, match="length"):
+            P.cache.status()
+        assert torch.equal(got, want) and torch.equal(P.k, wk) and torch.equal(P.v, wv), bad
