@@ -41,6 +41,11 @@ __device__ __forceinline__ int seq_of_row(const int32_t *row_start, int seqs, in
     return *first >= 0 && row >= *first && row < row_start[b + 1] ? b : -1;
 }
 
+// Whether the starts cover the pass: from row 0 to its last. One thread of a launch calls it.
+__device__ __forceinline__ void check_ends(const int32_t *row_start, int seqs, int rows, uint32_t *flags) {
+    if (row_start[0] != 0 || row_start[seqs] != rows) raise_flag(flags, MOE_FLAG_ROWS);
+}
+
 // Rows of sequence b, bounded to the pass: [first, first + returned count).
 __device__ __forceinline__ int seq_rows(const int32_t *row_start, int b, int rows, int *first, uint32_t *flags) {
     const int s = uniform(row_start[b]), e = uniform(row_start[b + 1]);

@@ -37,6 +37,7 @@ template <bool F16, bool HALF, int W>
 __global__ void __launch_bounds__(256) moe_rope_kernel(RopeParams p) {
     __shared__ float2 cs[128];
     const int row = (int)blockIdx.x, tid = (int)threadIdx.x;
+    const int end = p.row_start[p.c.seqs];
     int first = 0;
     const int b = seq_of_row(p.row_start, p.c.seqs, row, &first);
     if (b < 0) {
@@ -61,6 +62,8 @@ __global__ void __launch_bounds__(256) moe_rope_kernel(RopeParams p) {
         ok = page >= 0 && page < p.c.pages;
     }
     if (!ok && tid == 0) raise_flag(p.c.flags, len_ok ? MOE_FLAG_PAGE : MOE_FLAG_LEN);
+    // rows before the first start or past the last are met above; here a sequence that goes on past the pass
+    if (row == 0 && tid == 0 && end != p.rows) raise_flag(p.c.flags, MOE_FLAG_ROWS);
     __syncthreads();
 
     const int D = p.c.dim, rd = 2 * p.pairs;
@@ -145,6 +148,7 @@ constexpr int KEEP_STEP = 8, KEEP_CHUNK = 256;
 __global__ void __launch_bounds__(KEEP_CHUNK) moe_keep_kernel(KeepParams p) {
     __shared__ int4 moves[KEEP_CHUNK];    // of a chunk of the path: page and slot from, page and slot to; page -1: it stays
     const int b = (int)blockIdx.x, tid = (int)threadIdx.x;
+    if (b == 0 && tid == 64) check_ends(p.row_start, p.c.seqs, p.rows, p.c.flags);
     int first = 0;
     const int n = seq_rows(p.row_start, b, p.rows, &first, p.c.flags);
     const int len = p.c.len[b], keep = p.n_keep[b];

@@ -464,6 +464,7 @@ template <typename L> __global__ void __launch_bounds__(1024) moe_verify_walk_ke
     const int n = seq_rows(p.row_start, b, p.rows, &first, p.flags);
     WalkState &out = p.state[b];
     if (tid == 0) p.arrived[b] = 0;
+    if (b == 0 && tid == 1023) check_ends(p.row_start, p.seqs, p.rows, p.flags);
     if (n == 0) {
         if (tid == 0) {
             p.n_keep[b] = 0;

@@ -717,3 +717,23 @@ def test_append_with_a_bad_length_writes_nothing():
         with pytest.raises(B.MoeError, match="length"):
             P.cache.status()
         assert torch.equal(got, want) and torch.equal(P.k, wk) and torch.equal(P.v, wv), bad
+
+
+@pytest.mark.parametrize("bad", [[1, 4, 7], [0, 4, 6], [0, 4, 8], [2, 2, 7], [0, 0, 0]])
+def test_starts_that_do_not_cover_the_rows_are_reported(bad):
+    """row_start that does not begin at 0 or does not end at the number of rows, by every operator of the step."""
+    P = Paged([40, 20], [4, 3], 1, 64, 16, torch.bfloat16, seed=3)
+    q = torch.randn((7, 64), generator=_gen(1)).to(torch.bfloat16).cuda()
+    rope, starts = D.Rope(D.rope_frequencies(64)[0]), _i32(bad)
+    z, u, tokens = torch.randn((7, 300), generator=_gen(2)).cuda(), torch.full((7,), 0.5, device="cuda"), _i32([1] * 7)
+    v = D.Verifier(300, max_rows=7, max_seqs=2)
+    none = _i32([0, 0])
+    for status, call in ((P.cache.status, lambda: P.cache.append(rope, q, q, q, starts)),
+                         (P.cache.status, lambda: P.cache.attend(q, starts)),
+                         (P.cache.status, lambda: P.cache.keep(starts, none, tokens, new_len=_i32([0, 0]))),
+                         (v.status, lambda: v.verify(z, tokens, starts, None, u)),
+                         (v.status, lambda: v.verify(z, tokens, starts, u, u, draft_probs=torch.softmax(z, 1)))):
+        call()
+        with pytest.raises(B.MoeError, match="row_start"):
+            status()
+        status()
