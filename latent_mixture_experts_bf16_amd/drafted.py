@@ -14,8 +14,8 @@ chain, or a tree) through the model at once. Row 0 of a sequence is the certain 
     cache.keep(row_start, n_keep, path)              # once per layer's cache
 
 torch holds the memory and names the stream; every computation runs in the library's HIP kernels
-(include/moe_drafted.h states what each computes). Calls check their tensors, enqueue on the
-current stream of torch and return; they can be captured in a HIP graph. What only the
+(include/moe_drafted.h states what each computes). Calls check their tensors, enqueue on torch's
+current stream of the tensors' device and return; they can be captured in a HIP graph. What only the
 device can see is checked there and reported by status().
 """
 from __future__ import annotations
@@ -33,6 +33,7 @@ _DT = {torch.bfloat16: B.MOE_DT_BF16, torch.float16: B.MOE_DT_F16, torch.float32
        torch.int32: B.MOE_DT_I32}
 _LAYOUT = {"half": B.MOE_ROPE_HALF, "interleaved": B.MOE_ROPE_INTERLEAVED}
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
 def _refuse(status: int, message: str):
@@ -65,6 +66,16 @@ class _Caller:
             _refuse(_DEVICE, f"tensors on {self.device}: the kernels need a GPU")
         return _raw_stream(self.index) if _raw_stream else torch.cuda.current_stream(self.device).cuda_stream
 
+    def _launch(self, call, *args) -> None:
+        """call(*args, stream) of the library on the tensors' device, made the current one where it is not; raises
+        what it refuses."""
+        stream = self._stream()
+        if _current_device() == self.index:
+            B._check(call(*args, stream))
+        else:
+            with torch.cuda.device(self.index):
+                B._check(call(*args, stream))
+
     def _vector(self, name: str, t: torch.Tensor, dtype: torch.dtype, n: int) -> int:
         """The address of a contiguous vector of n elements."""
         if t.dtype != dtype:
@@ -93,7 +104,7 @@ class _Caller:
     def status(self) -> None:
         """Wait for the current stream's work; raise MOE_ERR_DEVICE_CHECK if a call since the last status()
         met something wrong on the device (a page outside the cache, a path out of order, ...)."""
-        B._check(_LIB.moe_drafted_status(self._flags_ptr, self._stream()))
+        self._launch(_LIB.moe_drafted_status, self._flags_ptr)
 
 
 class Rope:
@@ -211,8 +222,7 @@ class PagedCache(_Caller):
         if out is None:
             out = torch.empty((rows, heads * self.dim), dtype=self.dtype, device=self.device)
         op, os_ = self._matrix("out", out, self.dtype, rows, heads * self.dim)
-        B._check(_LIB.moe_rope_append(self._ref, rope._ref, rows, qp, qs, heads, kp, ks, vp, vs, sp, pp, op, os_,
-                                      self._stream()))
+        self._launch(_LIB.moe_rope_append, self._ref, rope._ref, rows, qp, qs, heads, kp, ks, vp, vs, sp, pp, op, os_)
         return out
 
     def attend(self, q: torch.Tensor, row_start: torch.Tensor, mask: Optional[torch.Tensor] = None,
@@ -233,9 +243,8 @@ class PagedCache(_Caller):
             B._check(-need)
         # from the stream's own pool each time, so that calls on several streams do not share it
         ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
-        B._check(_LIB.moe_tree_attend(self._ref, rows, qp, qs, heads, sp, mp,
-                                      self.dim ** -0.5 if scale is None else scale, op, os_,
-                                      ws.data_ptr() if need else None, need, self._stream()))
+        self._launch(_LIB.moe_tree_attend, self._ref, rows, qp, qs, heads, sp, mp,
+                     self.dim ** -0.5 if scale is None else scale, op, os_, ws.data_ptr() if need else None, need)
         return out
 
     def keep(self, row_start: torch.Tensor, n_keep: torch.Tensor, path: torch.Tensor,
@@ -252,7 +261,7 @@ class PagedCache(_Caller):
         if new_len is None:
             new_len = self.length
         lp = self._vector("new_len", new_len, torch.int32, self.seqs)
-        B._check(_LIB.moe_path_keep(self._ref, sp, rows, np_, pp, lp, self._stream()))
+        self._launch(_LIB.moe_path_keep, self._ref, sp, rows, np_, pp, lp)
         return new_len
 
 
@@ -307,7 +316,7 @@ class Verifier(_Caller):
         said = torch.empty(rows, dtype=torch.int32, device=self.device)
         logprobs = torch.empty(rows, dtype=torch.float32, device=self.device)
         ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
-        B._check(_LIB.moe_draft_verify(ctypes.byref(z), tp, sp, seqs, pp, ut, up, qp, qs, Tp, n_keep.data_ptr(),
-                                       path.data_ptr(), said.data_ptr(), logprobs.data_ptr(), self._flags_ptr,
-                                       ws.data_ptr() if need else None, need, self._stream()))
+        self._launch(_LIB.moe_draft_verify, ctypes.byref(z), tp, sp, seqs, pp, ut, up, qp, qs, Tp, n_keep.data_ptr(),
+                     path.data_ptr(), said.data_ptr(), logprobs.data_ptr(), self._flags_ptr,
+                     ws.data_ptr() if need else None, need)
         return n_keep, path, said, logprobs

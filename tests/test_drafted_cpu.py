@@ -253,3 +253,41 @@ def test_masks_and_depths():
     assert chain[62] == (1 << 63) - 1 and chain[63] == -1
     _refused("MOE_ERR_ROWS", "65 rows", D.tree_masks, list(range(-1, 64)))
     _refused("MOE_ERR_INVALID_ARG", "parent", D.tree_masks, [-1, 1])
+
+
+def test_calls_go_to_the_device_of_the_tensors(monkeypatch):
+    """Every call of the library is made with the tensors' device as the current one, whichever was, on its stream."""
+    now, seen = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+
+        def __exit__(self, *a):
+            now[0] = self.before
+
+    monkeypatch.setattr(D, "_raw_stream", lambda index: 100 + index)
+    monkeypatch.setattr(D, "_current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    c = D._Caller(torch.device("cpu"))
+    for c.index in (0, 1, 3):
+        c._launch(lambda *a: seen.append((now[0], a)) or 0, "x")
+        assert now[0] == 0
+        _refused("MOE_ERR_ROWS", "", c._launch, lambda *a: 10)
+        assert now[0] == 0
+    assert seen == [(0, ("x", 100)), (1, ("x", 101)), (3, ("x", 103))]
+
+    made = []
+    monkeypatch.setattr(D._Caller, "_launch", lambda self, call, *a: made.append(call.__name__))
+    cache, q, kv = _host_cache(), torch.zeros(4, 256, dtype=torch.bfloat16), torch.zeros(4, 128, dtype=torch.bfloat16)
+    i, f, starts = torch.zeros(4, dtype=torch.int32), torch.zeros(4), torch.tensor([0, 1, 2, 4], dtype=torch.int32)
+    cache.append(D.Rope([1.0] * 32, device="cpu"), q, kv, kv, starts)
+    cache.attend(q, starts)
+    cache.keep(starts, i[:3], i)
+    cache.status()
+    v = D.Verifier(100, max_rows=4, max_seqs=3, device="cpu")
+    v.verify(torch.zeros(4, 100), i, starts, f, f)
+    assert made == ["moe_rope_append", "moe_tree_attend", "moe_path_keep", "moe_drafted_status", "moe_draft_verify"]
