@@ -141,9 +141,10 @@ int64_t moe_draft_verify_workspace(int32_t rows, int32_t seqs, int32_t vocab);
 
 /* Move the kept rows' keys and values together: cached token len[b] + i becomes what token
  * len[b] + path[row_start[b] + i] was, for i < n_keep[b]; new_len[b] = len[b] + n_keep[b] (new_len
- * may be the cache's len). A path ascends strictly; one that does not, or leaves its sequence's rows,
- * moves nothing, sets MOE_FLAG_PATH and leaves the length as it was; so does, with MOE_FLAG_PAGE, one
- * of whose moved rows comes from or goes to a page outside the cache or past the table. */
+ * may be the cache's len; of layers whose caches share one, that of the last call alone). A path ascends
+ * strictly; one that does not, or leaves its sequence's rows, moves nothing, sets MOE_FLAG_PATH and leaves
+ * the length as it was; so does, with MOE_FLAG_PAGE, one of whose moved rows comes from or goes to a page
+ * outside the cache or past the table. */
 int moe_path_keep(const moe_paged_cache *c, const int32_t *row_start, int32_t rows, const int32_t *n_keep,
                   const int32_t *path, int32_t *new_len, void *hip_stream);
 

@@ -11,7 +11,7 @@ chain, or a tree) through the model at once. Row 0 of a sequence is the certain 
     ... the rest of the layers, logits ...
     n_keep, path, tokens, logprobs = verifier.verify(logits, drafted, row_start, u_test, u_pick,
                                                      parent=parent, draft_probs=probs)
-    cache.keep(row_start, n_keep, path)              # once per layer's cache
+    keep_paths(caches, row_start, n_keep, path)      # of all layers, whose lengths may be one tensor
 
 torch holds the memory and names the stream; every computation runs in the library's HIP kernels
 (include/moe_drafted.h states what each computes). Calls check their tensors, enqueue on torch's
@@ -251,7 +251,8 @@ class PagedCache(_Caller):
              new_len: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Move the accepted path together (n_keep [seqs], path [rows] as verify() gives them): cached
         token length[b] + i becomes row path[i]'s. new_len [seqs] gets length + n_keep (None: the
-        cache's own length does)."""
+        cache's own length does; where other layers' caches have the same length tensor, they would then
+        find it advanced: keep_paths() serves them all)."""
         sp = self._vector("row_start", row_start, torch.int32, self.seqs + 1)
         np_ = self._vector("n_keep", n_keep, torch.int32, self.seqs)
         if path.dim() != 1:
@@ -263,6 +264,20 @@ class PagedCache(_Caller):
         lp = self._vector("new_len", new_len, torch.int32, self.seqs)
         self._launch(_LIB.moe_path_keep, self._ref, sp, rows, np_, pp, lp)
         return new_len
+
+
+def keep_paths(caches: Sequence[PagedCache], row_start: torch.Tensor, n_keep: torch.Tensor, path: torch.Tensor) -> None:
+    """PagedCache.keep() of every layer's cache. A length tensor that several of them have is advanced once, by the
+    last, so that each finds the lengths of before the step."""
+    last = {c.length.data_ptr(): i for i, c in enumerate(caches)}
+    aside = None
+    for i, c in enumerate(caches):
+        new_len = None
+        if last[c.length.data_ptr()] != i:
+            if aside is None or aside.shape != c.length.shape or aside.device != c.device:
+                aside = torch.empty_like(c.length)
+            new_len = aside
+        c.keep(row_start, n_keep, path, new_len=new_len)
 
 
 class Verifier(_Caller):

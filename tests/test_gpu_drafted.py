@@ -737,3 +737,29 @@ def test_starts_that_do_not_cover_the_rows_are_reported(bad):
         with pytest.raises(B.MoeError, match="row_start"):
             status()
         status()
+
+
+def test_keep_of_layers_that_share_lengths():
+    """Three layers' caches over one table and one length tensor, and one with a length of its own: each moves its own
+    rows from where they were, and every length advances once."""
+    lens, rows = [40, 0, 15], [6, 4, 9]
+    layers = [Paged(lens, rows, 2, 64, 16, torch.bfloat16, seed=3) for _ in range(4)]
+    shared, own = layers[0], layers[3]
+    for j, P in enumerate(layers[1:3]):
+        P.k.copy_(torch.randn(P.k.shape, generator=_gen(50 + j)))
+        P.cache = D.PagedCache(P.k, P.v, shared.table, shared.len)
+    path = [[0, 2, 5], [0, 1], [0, 3, 4, 8]]
+    flat = [x for p, n in zip(path, rows) for x in p + [-1] * (n - len(p))]
+    want = []
+    for P in layers:
+        k, v = P.k.clone(), P.v.clone()
+        for b, p in enumerate(path):
+            for i, s in enumerate(p):
+                k[P.place(b, lens[b] + i)] = P.k[P.place(b, lens[b] + s)]
+                v[P.place(b, lens[b] + i)] = P.v[P.place(b, lens[b] + s)]
+        want.append((k, v))
+    D.keep_paths([P.cache for P in layers], _i32(_starts(rows)), _i32([len(p) for p in path]), _i32(flat))
+    for P, (k, v) in zip(layers, want):
+        P.cache.status()
+        assert torch.equal(P.k, k) and torch.equal(P.v, v)
+    assert shared.len.tolist() == own.len.tolist() == [43, 2, 19]
