@@ -99,7 +99,7 @@ class _Caller:
         stride, last = t.stride()
         if last != 1 and width > 1:
             _refuse(_LAYOUT_ERR, f"{name}: columns not contiguous")
-        return t.data_ptr(), stride if rows > 1 else max(stride, width)
+        return t.data_ptr(), stride if rows > 1 else width      # that of a single row means nothing
 
     def status(self) -> None:
         """Wait for the current stream's work; raise MOE_ERR_DEVICE_CHECK if a call since the last status()

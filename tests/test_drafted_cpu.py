@@ -291,3 +291,12 @@ def test_calls_go_to_the_device_of_the_tensors(monkeypatch):
     v = D.Verifier(100, max_rows=4, max_seqs=3, device="cpu")
     v.verify(torch.zeros(4, 100), i, starts, f, f)
     assert made == ["moe_rope_append", "moe_tree_attend", "moe_path_keep", "moe_drafted_status", "moe_draft_verify"]
+
+
+@pytest.mark.parametrize("width", [1, 64, 256])
+def test_the_stride_of_a_single_row_means_nothing(width):
+    """One row cut out of a wider, oddly strided matrix is taken as it lies; of two rows the stride is theirs."""
+    x = torch.zeros(3, 1001, dtype=torch.bfloat16)
+    c = D._Caller(torch.device("cpu"))
+    assert c._matrix("q", x[1:2, 8:8 + width], torch.bfloat16, 1, width) == (x.data_ptr() + 2 * 1009, width)
+    assert c._matrix("q", x[1:, :width], torch.bfloat16, 2, width) == (x.data_ptr() + 2 * 1001, 1001)

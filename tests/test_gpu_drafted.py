@@ -763,3 +763,16 @@ def test_keep_of_layers_that_share_lengths():
         P.cache.status()
         assert torch.equal(P.k, k) and torch.equal(P.v, v)
     assert shared.len.tolist() == own.len.tolist() == [43, 2, 19]
+
+
+def test_one_row_of_an_odd_stride():
+    """A single row cut out of rows that are not aligned to each other: aligned itself, so it is taken."""
+    P = Paged([37], [1], 2, 64, 16, torch.bfloat16, seed=6)
+    x = torch.randn((2, 1001), generator=_gen(1)).to(torch.bfloat16).cuda()
+    q, starts = x[:1, :256], _i32([0, 1])
+    rope = D.Rope(D.rope_frequencies(64)[0], layout="interleaved")
+    want = P.cache.append(rope, q.contiguous(), x[:1, 256:384].contiguous(), x[:1, 384:512].contiguous(), starts)
+    k = P.k.clone()
+    assert torch.equal(P.cache.append(rope, q, x[:1, 256:384], x[:1, 384:512], starts), want) and torch.equal(P.k, k)
+    assert torch.equal(P.cache.attend(q, starts), P.cache.attend(q.contiguous(), starts))
+    P.cache.status()
