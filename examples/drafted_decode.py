@@ -82,7 +82,8 @@ def draft_tree(text, followers, wide=2, deep=3):
 
 
 def decode(model, prompts, n_new):
-    """Greedy continuation of each prompt by at least n_new tokens; returns the texts and the number of steps."""
+    """Greedy continuation of each prompt by n_new tokens (a few more where the last step's drafts were accepted);
+    returns the texts and the number of steps."""
     seqs = len(prompts)
     texts = [list(p) for p in prompts]
     cache = new_cache(seqs, max(map(len, texts)) + n_new + 16)
@@ -97,8 +98,9 @@ def decode(model, prompts, n_new):
     steps = 0
     while min(len(t) - len(p) for t, p in zip(texts, prompts)) < n_new:
         tokens, parents, masks, positions, starts = [], [], [], [], [0]
-        for t, f in zip(texts, followers):
-            tok, par = draft_tree(t, f)
+        for t, p, f in zip(texts, prompts, followers):
+            # a sequence that has its tokens passes no more rows while the others go on
+            tok, par = draft_tree(t, f) if len(t) - len(p) < n_new else ([], [])
             tokens += tok
             parents += par
             masks += drafted.tree_masks(par)

@@ -40,3 +40,13 @@ def test_drafted_decoding_equals_plain_decoding():
             if i >= len(p) - 1:
                 assert float(z.max() - z[t[i + 1]]) <= 2 * 8 * 2.0 ** -8 * float(z.square().mean().sqrt()), i
         cache.status()
+
+
+def test_a_sequence_ahead_of_the_others_stays_in_its_cache():
+    """Sequences whose drafts are accepted more often have their tokens first; they wait for the others then."""
+    ex = _example()
+    torch.manual_seed(1)
+    prompts = [[5, 17, 200], [9], [31, 44, 7, 12, 90]]
+    texts, _ = ex.decode(ex.Model(vocab=256, seed=3), prompts, 120)
+    # the last step's path has at most three accepted drafts
+    assert all(120 <= len(t) - len(p) <= 123 for t, p in zip(texts, prompts))
