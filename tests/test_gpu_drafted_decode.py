@@ -50,3 +50,31 @@ def test_a_sequence_ahead_of_the_others_stays_in_its_cache():
     texts, _ = ex.decode(ex.Model(vocab=256, seed=3), prompts, 120)
     # the last step's path has at most three accepted drafts
     assert all(120 <= len(t) - len(p) <= 123 for t, p in zip(texts, prompts))
+
+
+def test_accepted_and_moved_rows_leave_what_plain_decoding_sees(monkeypatch):
+    """The same over 120 tokens, in which drafts are accepted and rows that are not in their place are moved there."""
+    ex = _example()
+    torch.manual_seed(1)
+    model, kept = ex.Model(vocab=256, seed=3), []
+    keep = ex.drafted.PagedCache.keep
+
+    def noting(self, row_start, n_keep, path, new_len=None):
+        kept.append((row_start.tolist(), n_keep.tolist(), path.tolist()))
+        return keep(self, row_start, n_keep, path, new_len=new_len)
+
+    monkeypatch.setattr(ex.drafted.PagedCache, "keep", noting)
+    prompts = [[5, 17, 200], [9], [31, 44, 7, 12, 90]]
+    texts, steps = ex.decode(model, prompts, 120)
+    # every step gives one token at least; more come from accepted drafts alone
+    accepted = sum(k - 1 for _, n, _ in kept for k in n if k)
+    assert accepted >= 12 and steps < 120 and steps == len(kept)
+    assert sum(path[at + i] != i for start, n, path in kept for at, k in zip(start, n) for i in range(k)) > 0
+    for t, p in zip(texts, prompts):
+        cache = ex.new_cache(1, len(t) + 1)
+        for i in range(len(t) - 1):
+            z = model.step(cache, ex.i32([t[i]]), ex.i32([0, 1]), None, None)[0].double()
+            cache.length.add_(1)
+            if i >= len(p) - 1:
+                assert float(z.max() - z[t[i + 1]]) <= 2 * 8 * 2.0 ** -8 * float(z.square().mean().sqrt()), i
+        cache.status()
