@@ -27,7 +27,6 @@ LIB_PATH = os.environ.get("MOE_LATENT_LIB") or os.path.join(_PKG, "libmoe_latent
 MOE_DT_BF16, MOE_DT_F16, MOE_DT_F32, MOE_DT_U32, MOE_DT_I32 = 1, 2, 3, 4, 5
 MOE_ACT_RELU2 = 1
 MOE_ROPE_HALF, MOE_ROPE_INTERLEAVED = 1, 2
-FLAG = {"page": 1, "len": 2, "rows": 4, "path": 8, "token": 16, "logits": 32}
 STATUS = {
     0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_TOPK_GT_EXPERTS", 3: "MOE_ERR_GROUPS",
     4: "MOE_ERR_SHAPE", 5: "MOE_ERR_MISSING_TENSOR", 6: "MOE_ERR_DTYPE", 7: "MOE_ERR_LAYOUT",

@@ -58,16 +58,6 @@ __device__ __forceinline__ int seq_rows(const int32_t *row_start, int b, int row
     return e - s;
 }
 
-// Cached length of sequence b, bounded to what the page table has room for.
-__device__ __forceinline__ int seq_len(const CacheParams &c, int b) {
-    const int n = uniform(c.len[b]);
-    if (n < 0 || n > c.cap) {
-        if (lane_id() == 0) raise_flag(c.flags, MOE_FLAG_LEN);
-        return n < 0 ? 0 : c.cap;
-    }
-    return n;
-}
-
 // Page and slot of token t of sequence b: false (and a flag) where the cache has no such token.
 __device__ __forceinline__ bool find_slot(const CacheParams &c, int b, int64_t t, int *page, int *slot) {
     bool ok = t >= 0 && t < c.cap;

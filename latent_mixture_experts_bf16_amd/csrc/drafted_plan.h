@@ -22,7 +22,7 @@ struct CacheParams {
     const int32_t *table, *len;
     uint32_t *flags;
     int64_t table_stride;
-    int32_t pages, page, heads, dim, seqs, width;
+    int32_t pages, page, heads, dim, seqs;
     int32_t cap;                // tokens the table has room for (at most 2^31 - 64)
 };
 
@@ -44,7 +44,8 @@ constexpr int attend_blocks(int dim, int queries) {
     return dim <= 64 ? (queries == 16 ? 4 : queries == 128 ? 2 : 3) : dim <= 96 ? 3 : dim <= 128 ? 2 : 1;
 }
 
-constexpr int ATTEND_MOST_RANGES = 1024;
+constexpr int COMPUTE_UNITS = 256;      // of an MI355X: workspaces are sized without asking a device
+constexpr int ATTEND_MOST_RANGES = COMPUTE_UNITS * attend_blocks(32, 16);
 
 // The first part of an item of attention work that was cut between workgroups: written by the range
 // that holds it, read by the launch that joins the parts.

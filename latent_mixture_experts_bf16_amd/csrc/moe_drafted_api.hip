@@ -34,25 +34,21 @@ static const char *type_name(int dt) {
     }
 }
 
-// Compute units of the current device, which must be gfx950. Asked of the runtime once per device.
-static int device_cus(int *cus) {
+// MOE_OK where the current device is a gfx950. Asked of the runtime once per device.
+static int check_device() {
     constexpr int MOST = 64;
-    static std::atomic<int> known[MOST];
+    static std::atomic<bool> known[MOST];
     int dev = -1;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess || dev < 0) return api_fail(MOE_ERR_DEVICE, "no HIP device (%s)", hipGetErrorString(e));
-    int n = dev < MOST ? known[dev].load(std::memory_order_relaxed) : 0;
-    if (!n) {
-        hipDeviceProp_t prop;
-        if ((e = hipGetDeviceProperties(&prop, dev)) != hipSuccess)
-            return api_fail(MOE_ERR_DEVICE, "hipGetDeviceProperties: %s", hipGetErrorString(e));
-        if (strncmp(prop.gcnArchName, "gfx950", 6) != 0)
-            return api_fail(MOE_ERR_DEVICE, "device %d is %s; this library is built for gfx950 (MI355X)", dev,
-                            prop.gcnArchName);
-        n = prop.multiProcessorCount;
-        if (dev < MOST) known[dev].store(n, std::memory_order_relaxed);
-    }
-    *cus = n;
+    if (dev < MOST && known[dev].load(std::memory_order_relaxed)) return MOE_OK;
+    hipDeviceProp_t prop;
+    if ((e = hipGetDeviceProperties(&prop, dev)) != hipSuccess)
+        return api_fail(MOE_ERR_DEVICE, "hipGetDeviceProperties: %s", hipGetErrorString(e));
+    if (strncmp(prop.gcnArchName, "gfx950", 6) != 0)
+        return api_fail(MOE_ERR_DEVICE, "device %d is %s; this library is built for gfx950 (MI355X)", dev,
+                        prop.gcnArchName);
+    if (dev < MOST) known[dev].store(true, std::memory_order_relaxed);
     return MOE_OK;
 }
 
@@ -151,7 +147,6 @@ static int check_cache(const moe_paged_cache *c, CacheParams &p) {
     p.heads = (int32_t)c->k.shape[2];
     p.dim = (int32_t)c->k.shape[3];
     p.seqs = (int32_t)seqs;
-    p.width = (int32_t)c->table.shape[1];
     const int64_t cap = c->table.shape[1] * c->k.shape[1], most = ((int64_t)1 << 31) - 64;
     p.cap = (int32_t)(cap < most ? cap : most);
     return MOE_OK;
@@ -226,7 +221,7 @@ extern "C" int moe_rope_append(const moe_paged_cache *c, const moe_rope *r, int3
     api_clear();
     RopeParams p;
     memset(&p, 0, sizeof p);
-    int rc, cus;
+    int rc;
     if ((rc = check_cache(c, p.c)) || (rc = check_rows(rows, q_heads, p.c))) return rc;
     if (!r) return api_fail(MOE_ERR_INVALID_ARG, "rope: NULL");
     if ((rc = check_words("rope freqs", r->freqs, 8))) return rc;
@@ -254,7 +249,7 @@ extern "C" int moe_rope_append(const moe_paged_cache *c, const moe_rope *r, int3
     const int w = odd % 8 == 0 ? 8 : odd % 4 == 0 ? 4 : odd % 2 == 0 ? 2 : 1;
     if (w == 1 && !half)
         return api_fail(MOE_ERR_LAYOUT, "interleaved pairs need rows aligned to 4 bytes");
-    if ((rc = device_cus(&cus))) return rc;
+    if ((rc = check_device())) return rc;
     p.freqs = r->freqs;
     p.pairs = r->pairs;
     p.magnitude = r->magnitude;
@@ -317,8 +312,7 @@ static AttendShape attend_shape(const CacheParams &c, int32_t rows, int32_t q_he
     // heads a key head, mean 56: the main launch 87 us with 64, 109 with 128, before items' starts counted as work.)
     const int64_t mean = ((int64_t)rows * (q_heads / c.heads) + c.seqs - 1) / c.seqs;
     s.queries = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
-    static_assert(256 * attend_blocks(32, 16) <= ATTEND_MOST_RANGES, "");
-    s.ranges = 256 * attend_blocks(c.dim, s.queries);     // as many workgroups as 256 compute units hold at once
+    s.ranges = COMPUTE_UNITS * attend_blocks(c.dim, s.queries);     // as many workgroups as the card holds at once
     s.stat = (int64_t)s.ranges * sizeof(AttendPart);
     s.sum = s.stat + (int64_t)s.ranges * 2 * 2 * s.queries * 4;
     s.bytes = s.sum + (int64_t)s.ranges * 2 * s.queries * c.dim * 4;
@@ -340,7 +334,7 @@ extern "C" int moe_tree_attend(const moe_paged_cache *c, int32_t rows, const voi
     api_clear();
     AttendParams p;
     memset(&p, 0, sizeof p);
-    int rc, cus;
+    int rc;
     if ((rc = check_cache(c, p.c)) || (rc = check_rows(rows, q_heads, p.c))) return rc;
     const int64_t w = (int64_t)q_heads * p.c.dim;
     if ((rc = check_matrix("q", q, q_stride, w, 16)) || (rc = check_matrix("out", out, out_stride, w, 16)) ||
@@ -351,7 +345,7 @@ extern "C" int moe_tree_attend(const moe_paged_cache *c, int32_t rows, const voi
     if (rows_overlap(out, out_stride, w, q, q_stride, w, rows))
         return api_fail(MOE_ERR_ALIAS, "out overlaps q");
     const AttendShape shape = attend_shape(p.c, rows, q_heads);
-    if ((rc = check_workspace(workspace, workspace_bytes, shape.bytes)) || (rc = device_cus(&cus))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, shape.bytes)) || (rc = check_device())) return rc;
     p.q = (const uint16_t *)q;
     p.out = (uint16_t *)out;
     p.q_stride = q_stride;
@@ -448,7 +442,7 @@ extern "C" int moe_draft_verify(const moe_tensor *logits, const int32_t *tokens,
                                 int32_t *n_keep, int32_t *path, int32_t *out_tokens, float *logprobs, uint32_t *flags,
                                 void *workspace, size_t workspace_bytes, void *hip_stream) {
     api_clear();
-    int rc, cus;
+    int rc;
     if (!logits) return api_fail(MOE_ERR_INVALID_ARG, "logits: descriptor is NULL");
     if (!logits->data) return api_fail(MOE_ERR_MISSING_TENSOR, "logits: missing (data == NULL)");
     if (logits->dtype != MOE_DT_F32 && logits->dtype != MOE_DT_BF16 && logits->dtype != MOE_DT_F16)
@@ -475,7 +469,7 @@ extern "C" int moe_draft_verify(const moe_tensor *logits, const int32_t *tokens,
                             (long long)vocab);
     }
     if ((rc = check_workspace(workspace, workspace_bytes, verify_layout(rows, seqs, vocab, nullptr, nullptr))) ||
-        (rc = device_cus(&cus)))
+        (rc = check_device()))
         return rc;
     VerifyParams p;
     memset(&p, 0, sizeof p);
@@ -510,12 +504,12 @@ extern "C" int moe_path_keep(const moe_paged_cache *c, const int32_t *row_start,
     api_clear();
     KeepParams p;
     memset(&p, 0, sizeof p);
-    int rc, cus;
+    int rc;
     if ((rc = check_cache(c, p.c)) || (rc = check_rows(rows, p.c.heads, p.c))) return rc;
     if ((rc = check_words("row_start", row_start)) || (rc = check_words("n_keep", n_keep)) ||
         (rc = check_words("path", path)) || (rc = check_words("new_len", new_len)))
         return rc;
-    if ((rc = device_cus(&cus))) return rc;
+    if ((rc = check_device())) return rc;
     p.row_start = row_start;
     p.n_keep = n_keep;
     p.path = path;
