@@ -114,15 +114,17 @@ int64_t moe_tree_attend_workspace(const moe_paged_cache *c, int32_t rows, int32_
  *     is drawn from max(p - S q, 0) (from p if that is all zero).
  *   without: the next token is drawn from p, and the walk goes to the first child that holds it.
  * A draw with u = u_pick[cur] takes the first index whose running sum passes u times the whole sum.
- * So tokens follow the target's distribution whatever the drafts. Probabilities and sums are
- * held in 64 bits. NaN logits count as -infinity.
+ * Without draft_probs tokens follow the target's distribution whatever the drafts; with them, where the drafts
+ * after a row were drawn from its q independently of each other (a token may then come twice). Drafts chosen otherwise
+ * (the most likely ones, or drawn without replacement) are for the form without. Probabilities and sums are held in
+ * 64 bits. NaN logits count as -infinity.
  *   logits       [rows][vocab] f32, bf16 or f16, rows at any stride >= vocab
  *   tokens       [rows] i32: the token each row holds (that of row 0 is not read); one outside
  *                the vocabulary is never accepted and changes nothing else
  *   parent       [rows] i32: a row's parent as its number within the sequence, less than its own;
  *                NULL: a chain
  *   u_test, u_pick  [rows] f32 in [0, 1) (u_test may be NULL without draft_probs)
- *   draft_probs  [rows][vocab] f32, or NULL: what the drafts after each row were drawn from
+ *   draft_probs  [rows][vocab] f32, or NULL: what the drafts after each row were drawn from, each for itself
  *   temperature  [seqs] f32, or NULL: 1
  *   n_keep       [seqs] i32: rows of the path, row 0 included
  *   path         [rows] i32: from row_start[b] on its rows, then -1

@@ -301,8 +301,8 @@ class Verifier(_Caller):
 
         logits [rows][vocab] f32, bf16 or f16; tokens [rows] i32, the token of each row; u_test, u_pick
         [rows] f32 in [0, 1); parent [rows] i32 within the sequence (None: a chain); draft_probs
-        [rows][vocab] f32, what the drafts after each row were drawn from (None: drafts chosen
-        without chance); temperature [seqs] f32 (None: 1; 0 or less: the largest logit).
+        [rows][vocab] f32, what the drafts after each row were drawn from, independently of each other (None:
+        drafts chosen in any other way); temperature [seqs] f32 (None: 1; 0 or less: the largest logit).
         Returns n_keep [seqs], path [rows], tokens [rows] i32 and logprobs [rows] f32: from
         row_start[b] on, the n_keep[b] rows of the path, the tokens after each, and their log
         probabilities; -1, -1 and 0 in the places after them."""
