@@ -49,7 +49,10 @@ template <bool F16> __device__ __forceinline__ f32x4 mfma16(s16x4 a, s16x4 b, f3
         return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(a, b, c, 0, 0, 0);
 }
 
-// Two probabilities rounded to the cache's type (to nearest even), the first in the low half.
+// Two elements rounded to the cache's type (to nearest even), the first in the low half: results, and the probabilities for
+// the product with V, since the matrix instructions take both operands in one type (fp32 ones do a sixteenth of the
+// work a cycle). Their sum is of the unrounded ones, in fp32. Against 64 bits the rms error of one row's result over 777
+// tokens is then 0.0020 of its size in bf16, where products of fp32 probabilities, rounded once, leave 0.0017.
 template <bool F16> __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const f32x2 v = {a, b};
     if constexpr (F16)
