@@ -494,7 +494,7 @@ template <typename L> __global__ void __launch_bounds__(1024) moe_verify_walk_ke
 }
 
 // Workgroup (b, y): sums of 4 chunks of sequence b's row, if it waits for them. 64 rows of 100003 logits and draft
-// probabilities (51 MB): 24 us, of which the last workgroups' walks and picks are about 10; one row of 131072: 13 us.
+// probabilities (51 MB): 22 us, of which the last workgroups' walks and picks are about 10; one row of 131072: 13 us.
 // Four waves at 128 registers leave four workgroups a compute unit (the walk spills some; eight waves at 151
 // registers took 28 us), and the sums go round the caches (device fences in every wave: 128 us).
 template <typename L> __global__ void __launch_bounds__(256, 4) moe_verify_left_kernel(VerifyParams p) {
