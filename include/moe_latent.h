@@ -31,7 +31,7 @@ extern "C" {
 #endif
 
 /* element types of moe_tensor.dtype and of the activation / router switches */
-enum moe_dtype { MOE_DT_BF16 = 1, MOE_DT_F16 = 2, MOE_DT_F32 = 3, MOE_DT_U32 = 4, MOE_DT_I32 = 5 };
+enum moe_dtype { MOE_DT_BF16 = 1, MOE_DT_F16 = 2, MOE_DT_F32 = 3, MOE_DT_U32 = 4, MOE_DT_I32 = 5, MOE_DT_U8 = 6 };
 
 /* expert activation (the only one the layer uses: relu^2 of the up projection) */
 enum moe_activation { MOE_ACT_RELU2 = 1 };

@@ -23,10 +23,11 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 # tests point it at a host-only build instrumented with AddressSanitizer and UBSan).
 LIB_PATH = os.environ.get("MOE_LATENT_LIB") or os.path.join(_PKG, "libmoe_latent.so")
 
-# enum values of include/moe_latent.h and include/moe_drafted.h
-MOE_DT_BF16, MOE_DT_F16, MOE_DT_F32, MOE_DT_U32, MOE_DT_I32 = 1, 2, 3, 4, 5
+# enum values of include/moe_latent.h, include/moe_drafted.h and include/moe_serving.h
+MOE_DT_BF16, MOE_DT_F16, MOE_DT_F32, MOE_DT_U32, MOE_DT_I32, MOE_DT_U8 = 1, 2, 3, 4, 5, 6
 MOE_ACT_RELU2 = 1
 MOE_ROPE_HALF, MOE_ROPE_INTERLEAVED = 1, 2
+MOE_MX8, MOE_MX4 = 1, 2
 STATUS = {
     0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_TOPK_GT_EXPERTS", 3: "MOE_ERR_GROUPS",
     4: "MOE_ERR_SHAPE", 5: "MOE_ERR_MISSING_TENSOR", 6: "MOE_ERR_DTYPE", 7: "MOE_ERR_LAYOUT",
@@ -65,6 +66,20 @@ class moe_paged_cache(ctypes.Structure):
 class moe_rope(ctypes.Structure):
     _fields_ = [("freqs", ctypes.c_void_p), ("pairs", ctypes.c_int32), ("layout", ctypes.c_int32),
                 ("magnitude", ctypes.c_float)]
+
+
+class moe_head_norm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("offset", ctypes.c_float)]
+
+
+class moe_mx_cache(ctypes.Structure):
+    _fields_ = [(n, moe_tensor) for n in ("k", "v", "k_scale", "v_scale", "table", "len")] + [
+        ("flags", ctypes.c_void_p), ("format", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class moe_shared_prefix(ctypes.Structure):
+    _fields_ = [("group_start", ctypes.c_void_p), ("len", ctypes.c_void_p), ("groups", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -114,6 +129,18 @@ def _load():
         "moe_draft_verify_workspace": (i64, [i32, i32, i32]),
         "moe_path_keep": (ctypes.c_int, [P, P, i32, P, P, P, P]),
         "moe_drafted_status": (ctypes.c_int, [P, P]),
+        # include/moe_serving.h
+        "moe_norm_rope_append": (ctypes.c_int, [P, P, P, i32, P, i64, i32, P, i64, P, i64, P, P, P, i64, P]),
+        "moe_mx_cache_check": (ctypes.c_int, [P]),
+        "moe_mx_append": (ctypes.c_int, [P, P, P, i32, P, i64, i32, P, i64, P, i64, P, P, P, i64, P]),
+        "moe_mx_read": (ctypes.c_int, [P, i32, P, P, P, i64, P, i64, P]),
+        "moe_mx_keep": (ctypes.c_int, [P, P, i32, P, P, P, P]),
+        "moe_mx_attend": (ctypes.c_int, [P, P, i32, P, i64, i32, P, P, ctypes.c_float, P, i64, P, ctypes.c_size_t, P]),
+        "moe_mx_attend_workspace": (i64, [P, i32, i32, i32]),
+        "moe_shared_attend": (ctypes.c_int, [P, P, i32, P, i64, i32, P, P, ctypes.c_float, P, i64, P, ctypes.c_size_t, P]),
+        "moe_shared_attend_workspace": (i64, [P, i32, i32, i32]),
+        "moe_sample": (ctypes.c_int, [P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]),
+        "moe_sample_workspace": (i64, [i32, i32]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -132,6 +159,10 @@ EXPORTED = ("moe_latent_create", "moe_latent_forward", "moe_latent_destroy", "mo
 # the functions of include/moe_drafted.h (drafted.py calls them)
 DRAFTED = ("moe_paged_cache_check", "moe_rope_append", "moe_tree_attend", "moe_tree_attend_workspace",
            "moe_draft_verify", "moe_draft_verify_workspace", "moe_path_keep", "moe_drafted_status")
+# the functions of include/moe_serving.h (serving.py and drafted.py call them)
+SERVING = ("moe_norm_rope_append", "moe_mx_cache_check", "moe_mx_append", "moe_mx_read", "moe_mx_keep", "moe_mx_attend",
+           "moe_mx_attend_workspace", "moe_shared_attend", "moe_shared_attend_workspace", "moe_sample",
+           "moe_sample_workspace")
 
 
 def lib():

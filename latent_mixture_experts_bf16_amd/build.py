@@ -13,7 +13,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmoe_latent.so")
 SOURCES = ["layer_kernels.hip", "prefill_kernels.hip", "moe_latent_api.hip", "drafted_kernels.hip",
-           "attend_kernels.hip", "verify_kernels.hip", "moe_drafted_api.hip"]
+           "attend_kernels.hip", "attend_shared_kernels.hip", "attend_mx8_kernels.hip", "attend_mx4_kernels.hip",
+           "attend_launch.hip", "verify_kernels.hip", "moe_drafted_api.hip", "serving_kernels.hip", "sample_kernels.hip",
+           "moe_serving_api.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

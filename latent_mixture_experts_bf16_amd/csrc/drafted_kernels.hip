@@ -1,4 +1,6 @@
 // drafted_kernels.hip -- rotary append and path keeping (gfx950).
+#include <type_traits>
+
 #include "drafted_items.h"
 
 namespace moe {
@@ -145,7 +147,10 @@ ROPE_KERNELS(true);
 // 24 rows take 5.5 us as a pass among others (7.2 where every thread looks the slots up for itself at each step), one 5.3.
 constexpr int KEEP_STEP = 8, KEEP_CHUNK = 256;
 
-__global__ void __launch_bounds__(KEEP_CHUNK) moe_keep_kernel(KeepParams p) {
+// A cache of codes (FMT) has strides in bytes, and its blocks' scales move with them.
+template <int FMT> __global__ void __launch_bounds__(KEEP_CHUNK) moe_keep_kernel(KeepParams p) {
+    typedef typename std::conditional<FMT == MX_NONE, uint16_t, uint8_t>::type T;
+    constexpr int PIECE = 16 / (int)sizeof(T);
     __shared__ int4 moves[KEEP_CHUNK];    // of a chunk of the path: page and slot from, page and slot to; page -1: it stays
     const int b = (int)blockIdx.x, tid = (int)threadIdx.x;
     if (b == 0 && tid == 64) check_ends(p.row_start, p.c.seqs, p.rows, p.c.flags);
@@ -179,7 +184,7 @@ __global__ void __launch_bounds__(KEEP_CHUNK) moe_keep_kernel(KeepParams p) {
         }
         return;
     }
-    const int per = p.c.dim / 8, heads = p.c.heads;
+    const int per = mx_row_bytes(FMT, p.c.dim) / 16, heads = p.c.heads;
     for (int c0 = 0; c0 < keep; c0 += KEEP_CHUNK) {
         const int here = min(KEEP_CHUNK, keep - c0);
         if (c0) {
@@ -190,9 +195,9 @@ __global__ void __launch_bounds__(KEEP_CHUNK) moe_keep_kernel(KeepParams p) {
         for (int u = tid; u < 2 * heads * per; u += KEEP_CHUNK) {
             const bool value = u >= heads * per;
             const int w = value ? u - heads * per : u;
-            const int h = w / per, d = (w - h * per) * 8;
+            const int h = w / per, d = (w - h * per) * PIECE;
             const KvView &kv = value ? p.c.v : p.c.k;
-            uint16_t *base = (uint16_t *)kv.p + h * kv.head + d;
+            T *base = (T *)kv.p + h * kv.head + d;
             for (int i0 = 0; i0 < here; i0 += KEEP_STEP) {
                 uint4 x[KEEP_STEP];
                 int64_t to[KEEP_STEP];
@@ -209,9 +214,25 @@ __global__ void __launch_bounds__(KEEP_CHUNK) moe_keep_kernel(KeepParams p) {
                     if (to[k] >= 0) *(uint4 *)(base + to[k]) = x[k];
             }
         }
+        if (FMT != MX_NONE) {
+            const int blocks = p.c.dim / 32;
+            for (int u = tid; u < 2 * heads * blocks; u += KEEP_CHUNK) {
+                const bool value = u >= heads * blocks;
+                const int w = value ? u - heads * blocks : u, h = w / blocks;
+                const ScaleView &sv = value ? p.c.vs : p.c.ks;
+                uint8_t *base = (uint8_t *)sv.p + h * sv.head + (w - h * blocks);
+                for (int i = 0; i < here; ++i) {
+                    const int4 m = moves[i];
+                    if (m.x >= 0) base[m.z * sv.page + m.w * sv.slot] = base[m.x * sv.page + m.y * sv.slot];
+                }
+            }
+        }
     }
     // every thread read the length before the barrier above, so the cache's own may be written
     if (tid == 0) p.new_len[b] = len + keep;
 }
+template __global__ void moe_keep_kernel<MX_NONE>(KeepParams);
+template __global__ void moe_keep_kernel<MX_E4M3>(KeepParams);
+template __global__ void moe_keep_kernel<MX_E2M1>(KeepParams);
 
 }  // namespace moe

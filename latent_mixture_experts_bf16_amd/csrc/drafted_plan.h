@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "moe_drafted.h"
+#include "moe_serving.h"
 
 namespace moe {
 
@@ -12,13 +13,27 @@ namespace moe {
 int api_fail(int code, const char *fmt, ...);
 void api_clear();
 
+// What a cache holds its values as.
+enum { MX_NONE = 0, MX_E4M3 = MOE_MX8, MX_E2M1 = MOE_MX4 };
+
+// Bytes of one head's values of a token.
+constexpr int mx_row_bytes(int format, int dim) {
+    return format == MX_NONE ? 2 * dim : format == MX_E4M3 ? dim : dim / 2;
+}
+
 struct KvView {
     const uint16_t *p;
-    int64_t page, slot, head;   // strides in elements
+    int64_t page, slot, head;   // strides in elements; of codes in bytes
+};
+
+struct ScaleView {
+    const uint8_t *p;
+    int64_t page, slot, head;
 };
 
 struct CacheParams {
     KvView k, v;
+    ScaleView ks, vs;           // of a cache of codes
     const int32_t *table, *len;
     uint32_t *flags;
     int64_t table_stride;
@@ -36,6 +51,25 @@ struct RopeParams {
     int64_t q_stride, k_stride, v_stride, qo_stride;
     const int32_t *row_start, *positions;
     int32_t rows, q_heads;
+};
+
+// Rows normed, rotated and appended (serving_kernels.hip).
+struct AppendParams {
+    RopeParams r;
+    const void *q_weight, *k_weight;
+    int64_t qw_stride, kw_stride;
+    int32_t norm;               // moe_dtype of the weights, 0: no norm
+    float eps, offset;
+    int32_t half, wide;         // layout; every row 16-byte aligned
+    int32_t lanes;              // that hold a head, eight dims each: a power of two
+};
+
+struct ReadParams {
+    CacheParams c;
+    const int32_t *row_start, *start;
+    uint16_t *k, *v;
+    int64_t k_stride, v_stride;
+    int32_t rows;
 };
 
 // Workgroups of the attention kernel that a compute unit holds at once: by LDS (two buffers of 64
@@ -67,7 +101,37 @@ struct AttendParams {
     AttendPart *parts;          // [ranges]
     float *part_stat;           // [2 ranges][2][tile_queries]: maximum, sum
     float *part_sum;            // [2 ranges][tile_queries][dim]
+    // a batch that shares prompts: entries of work (groups, then sequences), what its first launch is told, and what it
+    // leaves for the second
+    int32_t entries, groups;
+    const int32_t *group_start, *shared_len;    // NULL in the second launch
+    int32_t *skip_out;
+    const int32_t *skip;        // [seqs], NULL in the first launch
+    float *prior_stat;          // [rows][q_heads][2]: maximum, sum
+    float *prior_sum;           // [rows][q_heads][dim]
 };
+
+// A call of the attention operators whose cache is checked and in the parameters (attend_launch.hip checks the rest).
+struct AttendCall {
+    bool f16;
+    int format;
+    const moe_shared_prefix *shared;    // or NULL
+    int32_t rows;
+    const void *q;
+    int64_t q_stride;
+    int32_t q_heads;
+    const int32_t *row_start;
+    const uint64_t *mask;
+    float scale;
+    void *out;
+    int64_t out_stride;
+    void *workspace;
+    size_t workspace_bytes;
+    void *stream;
+};
+int64_t attend_workspace(const CacheParams &c, int32_t rows, int32_t q_heads, int32_t groups);
+int check_shared(const moe_shared_prefix *s, const CacheParams &c);
+int attend_run(const AttendCall &a, AttendParams &p);
 
 constexpr int MAX_VOCAB = 1 << 20;
 constexpr int VOCAB_CHUNK = 1024;   // logits of a row that one wave takes at a time
@@ -105,6 +169,28 @@ struct VerifyParams {
     WalkState *state;           // [seqs]
     uint32_t *arrived;          // [seqs]: workgroups that have added their part of a sum; apart from the state, which is
                                 // copied and stored whole
+};
+
+// Sampling (sample_kernels.hip). Logits of a row are taken in chunks; of each a histogram over cells of an eighth of an octave of
+// their weight, the same grid for all chunks of a row.
+constexpr int SAMPLE_CHUNK = 4096, SAMPLE_CELLS = 256;
+struct SampleHead {
+    double cell;                // of the largest logit
+    float top;                  // -infinity: nothing above that
+    uint32_t pad;
+};
+struct SampleParams {
+    const void *logits;
+    int64_t stride;
+    const float *u, *temperature, *top_p, *min_p;
+    const int32_t *top_k;
+    int32_t *tokens;
+    float *logprobs;
+    uint32_t *flags;
+    int32_t rows, vocab, chunks;
+    SampleHead *head;           // [rows][chunks]
+    uint64_t *mass;             // [rows][chunks][SAMPLE_CELLS], in 2^-50 of the chunk's largest weight
+    uint16_t *count;            // [rows][chunks][SAMPLE_CELLS]
 };
 
 struct KeepParams {

@@ -30,7 +30,7 @@ from . import binding as B
 
 _LIB = B.lib()
 _DT = {torch.bfloat16: B.MOE_DT_BF16, torch.float16: B.MOE_DT_F16, torch.float32: B.MOE_DT_F32,
-       torch.int32: B.MOE_DT_I32}
+       torch.int32: B.MOE_DT_I32, torch.uint8: B.MOE_DT_U8}
 _LAYOUT = {"half": B.MOE_ROPE_HALF, "interleaved": B.MOE_ROPE_INTERLEAVED}
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
@@ -203,13 +203,18 @@ class PagedCache(_Caller):
             _refuse(_SHAPE, f"{name}: {width} wide, not heads of {self.dim}")
         return rows, width // self.dim
 
+    # the calls of a cache of codes differ in these (serving.MxCache)
+    _append_call, _keep_call = _LIB.moe_norm_rope_append, _LIB.moe_path_keep
+
     def append(self, rope: Rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, row_start: torch.Tensor,
-               positions: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+               positions: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               norm: "Optional[HeadNorm]" = None) -> torch.Tensor:
         """Rotate the queries q [rows][heads * dim] into `out` (new if None; may be q) and the keys
         k [rows][kv_heads * dim] into the cache, and copy the values v there: row i of sequence b
         becomes cached token length[b] + i. positions [rows] i32 (None: length[b] + i). The cache's
         length does not change; keep() or the caller moves it. q, k and v may be column slices
-        of one projection's output."""
+        of one projection's output. norm: a serving.HeadNorm, applied to every head of q and k before it
+        turns, in the same pass."""
         rows, heads = self._heads("q", q)
         qp, qs = self._matrix("q", q, self.dtype, rows, heads * self.dim)
         kw = self.kv_heads * self.dim
@@ -222,15 +227,24 @@ class PagedCache(_Caller):
         if out is None:
             out = torch.empty((rows, heads * self.dim), dtype=self.dtype, device=self.device)
         op, os_ = self._matrix("out", out, self.dtype, rows, heads * self.dim)
-        self._launch(_LIB.moe_rope_append, self._ref, rope._ref, rows, qp, qs, heads, kp, ks, vp, vs, sp, pp, op, os_)
+        if norm is None and type(self) is PagedCache:
+            self._launch(_LIB.moe_rope_append, self._ref, rope._ref, rows, qp, qs, heads, kp, ks, vp, vs, sp, pp, op, os_)
+            return out
+        np_ = None
+        if norm is not None:
+            norm._check(self.device, self.index, heads, self.kv_heads, self.dim)
+            np_ = norm._ref
+        self._launch(self._append_call, self._ref, np_, rope._ref, rows, qp, qs, heads, kp, ks, vp, vs, sp, pp, op, os_)
         return out
 
     def attend(self, q: torch.Tensor, row_start: torch.Tensor, mask: Optional[torch.Tensor] = None,
-               scale: Optional[float] = None, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+               scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+               shared: "Optional[SharedPrefix]" = None) -> torch.Tensor:
         """Attention of the step's rows, after append(): row i of sequence b over the cached tokens
         and, of the step's rows, those with their bit set in mask [rows] i64 (None: rows 0 to i).
         q, out [rows][heads * dim]; scale: on the scores (None: dim ** -0.5). A row that sees
-        nothing gives zeros."""
+        nothing gives zeros. shared: a serving.SharedPrefix, the groups of sequences that begin with the same
+        tokens, which are then read once for all rows of a group."""
         rows, heads = self._heads("q", q)
         qp, qs = self._matrix("q", q, self.dtype, rows, heads * self.dim)
         sp = self._vector("row_start", row_start, torch.int32, self.seqs + 1)
@@ -238,14 +252,26 @@ class PagedCache(_Caller):
         if out is None:
             out = torch.empty((rows, heads * self.dim), dtype=self.dtype, device=self.device)
         op, os_ = self._matrix("out", out, self.dtype, rows, heads * self.dim)
-        need = _LIB.moe_tree_attend_workspace(self._ref, rows, heads)
+        if shared is not None:
+            shared._check(self.device, self.index, self.seqs)
+        need = self._attend_workspace(shared, rows, heads)
         if need < 0:
             B._check(-need)
         # from the stream's own pool each time, so that calls on several streams do not share it
         ws = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
-        self._launch(_LIB.moe_tree_attend, self._ref, rows, qp, qs, heads, sp, mp,
-                     self.dim ** -0.5 if scale is None else scale, op, os_, ws.data_ptr() if need else None, need)
+        self._attend(shared, rows, qp, qs, heads, sp, mp, self.dim ** -0.5 if scale is None else scale, op, os_,
+                     ws.data_ptr() if need else None, need)
         return out
+
+    def _attend_workspace(self, shared, rows: int, heads: int) -> int:
+        return (_LIB.moe_tree_attend_workspace(self._ref, rows, heads) if shared is None else
+                _LIB.moe_shared_attend_workspace(self._ref, shared.groups, rows, heads))
+
+    def _attend(self, shared, *args) -> None:
+        if shared is None:
+            self._launch(_LIB.moe_tree_attend, self._ref, *args)
+        else:
+            self._launch(_LIB.moe_shared_attend, self._ref, shared._ref, *args)
 
     def keep(self, row_start: torch.Tensor, n_keep: torch.Tensor, path: torch.Tensor,
              new_len: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -262,7 +288,7 @@ class PagedCache(_Caller):
         if new_len is None:
             new_len = self.length
         lp = self._vector("new_len", new_len, torch.int32, self.seqs)
-        self._launch(_LIB.moe_path_keep, self._ref, sp, rows, np_, pp, lp)
+        self._launch(self._keep_call, self._ref, sp, rows, np_, pp, lp)
         return new_len
 
 
