@@ -175,7 +175,7 @@ struct VerifyParams {
 // their weight, the same grid for all chunks of a row.
 constexpr int SAMPLE_CHUNK = 4096, SAMPLE_CELLS = 256;
 struct SampleHead {
-    double cell;                // of the largest logit
+    double top_y;               // the largest logit, in cells
     float top;                  // -infinity: nothing above that
     uint32_t pad;
 };

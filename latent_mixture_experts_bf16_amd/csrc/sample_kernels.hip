@@ -44,51 +44,75 @@ template <typename L> __device__ __forceinline__ float value_of(uint32_t key) {
     return O::value(key & O::SIGN ? key & ~O::SIGN : ~key & MASK);
 }
 
-// Temperature of a row: 1 / T, the cells of a logit, and whether only the largest logit counts. A greedy row is one that keeps
-// the first token of the order; its weights are then of no matter.
+// Temperature of a row as cells (eighths of an octave of weight) of a logit, and whether only the largest logit counts. A greedy
+// row is one that keeps the first token of the order; its weights are then of no matter. (An infinite T counts as the
+// largest finite one, so that a logit of -infinity still weighs nothing.)
 struct RowHeat {
-    double inv, cells;
+    double cells;
     bool greedy;
 };
 __device__ __forceinline__ RowHeat row_heat(const SampleParams &p, int row) {
     const float T = p.temperature ? p.temperature[row] : 1.0f;
     const bool greedy = !(T > 0.0f);
-    const double inv = greedy ? 1.0 : 1.0 / (double)fminf(T, 3.4028234e38f);
-    return {inv, inv * (8.0 * 1.4426950408889634), greedy};
+    return {(greedy ? 1.0 : 1.0 / (double)fminf(T, 3.4028234e38f)) * (8.0 * 1.4426950408889634), greedy};
 }
-// The cell of the grid that a logit lies in: rising with it.
-__device__ __forceinline__ double cell_of(float x, const RowHeat &h) { return floor((double)x * h.cells); }
-// How many cells below, 0 .. SAMPLE_CELLS - 1 (the last one holds all that lie further down).
+// How many cells below the one of the largest a cell is, 0 .. SAMPLE_CELLS - 1 (the last one holds all that lie further down).
 __device__ __forceinline__ int cells_below(double top, double cell) {
     const double d = top == cell ? 0.0 : top - cell;
     return d < (double)(SAMPLE_CELLS - 1) ? (int)d : SAMPLE_CELLS - 1;
 }
-// A weight as a whole number of 2^-shift.
-__device__ __forceinline__ uint64_t whole(double w, int shift) {
-    return (uint64_t)fma(w, __longlong_as_double((long long)(1023 + shift) << 52), 0.5);
+
+// 2^(y / 8) for y <= 0, to about 2^-48: y = n / 4 + r with |r| <= 1/8, 2^(n / 32) from a table (its entries lie on different
+// banks of LDS) and the exponent, times the Taylor polynomial of degree 5 of e^(r log(2) / 8) (its remainder is below
+// 3e-15 of the value where r is largest). n is rounded by adding 1.5 2^52, which leaves it in the low bits. Below 2^-64, where
+// nothing is left of it in what follows, 2^-64.
+__device__ __forceinline__ double weight_of(double y) {
+    constexpr double ROUND = 6755399441055744.0, C = 0.08664339756999316;     // log(2) / 8
+    y = fmax(y, -512.0);
+    const double t = fma(y, 4.0, ROUND);
+    const double r = fma(t - ROUND, -0.25, y);
+    const int k = (int)(uint32_t)(uint64_t)__double_as_longlong(t);
+    const double m = exp_table()[k & 31];
+    double e = fma(r, C * C * C * C * C / 120.0, C * C * C * C / 24.0);
+    e = fma(e, r, C * C * C / 6.0);
+    e = fma(e, r, C * C / 2.0);
+    e = fma(e, r, C);
+    e = fma(m, e * r, m);
+    const uint64_t bits = (uint64_t)__double_as_longlong(e) + ((uint64_t)(uint32_t)((k >> 5) * (1 << 20)) << 32);
+    return __longlong_as_double((long long)bits);
 }
+// The weight of a logit beside the largest, y and top_y in cells. Where the largest is infinite, all weight is on it.
+__device__ __forceinline__ double beside(double y, double top_y) {
+    return y == top_y ? 1.0 : top_y == __builtin_inf() ? 0.0 : weight_of(y - top_y);
+}
+// A weight of at most 1 as a whole number of 2^-50, to nearest: the low bits of its sum with 4.
+__device__ __forceinline__ uint64_t whole50(double w) {
+    return (uint64_t)__double_as_longlong(fma(w, 0x1p50, 0x1p52)) & 0xFFFFFFFFFFFFFull;
+}
+// A weight as a whole number of 2^-shift.
 __device__ __forceinline__ double power2(int e) { return __longlong_as_double((long long)(1023 + e) << 52); }
+__device__ __forceinline__ uint64_t whole(double w, int shift) { return (uint64_t)fma(w, power2(shift), 0.5); }
 
 template <typename L> __device__ __forceinline__ const typename L::T *row_of(const SampleParams &p, int row) {
     return (const typename L::T *)p.logits + (int64_t)row * p.stride;
 }
 
-// Add to a cell of a histogram in LDS. Where a wave's lanes all have the same one (rows of equal logits), once for all.
+// Add to a cell of a histogram in LDS. Where the lanes that do all have the same one (rows of equal logits), once for all.
 __device__ __forceinline__ void add_to(uint64_t *mass, uint32_t *count, int at, uint64_t w, bool on) {
-    const uint64_t who = __ballot(on);
-    if (!who) return;
-    const int one = __builtin_amdgcn_readlane(at, (int)__builtin_ctzll(who));
-    if (__ballot(on && at == one) == who && __popcll(who) > 8) {
-        uint64_t sum = on ? w : 0;
-        for (int d = 32; d; d >>= 1) sum += (uint64_t)__shfl_xor((long long)sum, d);
-        if (lane_id() == 0) {
-            atomicAdd((unsigned long long *)mass + one, (unsigned long long)sum);
-            atomicAdd(count + one, (uint32_t)__popcll(who));
+    if (!on) return;
+    if (__all(at == uniform(at))) {
+        const uint64_t who = __ballot(true);
+        if (__popcll(who) == 64) {
+            for (int d = 32; d; d >>= 1) w += (uint64_t)__shfl_xor((long long)w, d);
+            if (lane_id() == 0) {
+                atomicAdd((unsigned long long *)mass + at, (unsigned long long)w);
+                atomicAdd(count + at, 64u);
+            }
+            return;
         }
-    } else if (on) {
-        atomicAdd((unsigned long long *)mass + at, (unsigned long long)w);
-        atomicAdd(count + at, 1u);
     }
+    atomicAdd((unsigned long long *)mass + at, (unsigned long long)w);
+    atomicAdd(count + at, 1u);
 }
 
 // ------------------------------------------------------------------ the histogram of a chunk
@@ -115,14 +139,22 @@ template <typename L> __global__ void __launch_bounds__(256) moe_sample_cells_ke
     __syncthreads();
     top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
     const int64_t at = (int64_t)row * p.chunks + c;
-    const double cell = cell_of(top, h);
-    if (tid == 0) p.head[at] = {cell, top, 0};
+    const double top_y = (double)top * h.cells, cell = floor(top_y);
+    if (tid == 0) p.head[at] = {top_y, top, 0};
     if (!(top > -__builtin_inff())) return;
+    if (top < __builtin_inff()) {
 #pragma unroll
-    for (int k = 0; k < SHARE; ++k) {
-        const bool on = x[k] > -__builtin_inff();                // a NaN is not
-        const double w = on ? relative(x[k], top, h.inv) : 0.0;
-        add_to(mass, count, on ? cells_below(cell, cell_of(x[k], h)) : 0, whole(w, 50), on);
+        for (int k = 0; k < SHARE; ++k) {
+            const double y = (double)x[k] * h.cells;
+            const double d = fmin(cell - floor(y), (double)(SAMPLE_CELLS - 1));
+            add_to(mass, count, (int)d, whole50(weight_of(y - top_y)), x[k] > -__builtin_inff());     // a NaN is not
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < SHARE; ++k) {
+            const bool on = x[k] > -__builtin_inff(), is = x[k] == top;
+            add_to(mass, count, is ? 0 : SAMPLE_CELLS - 1, is ? 1ull << 50 : 0, on);
+        }
     }
     __syncthreads();
     p.mass[at * SAMPLE_CELLS + tid] = mass[tid];
@@ -131,65 +163,30 @@ template <typename L> __global__ void __launch_bounds__(256) moe_sample_cells_ke
 
 // ------------------------------------------------------------------ the row
 
-constexpr int ROW_THREADS = 1024, ROW_LIST = 8192, STEP_BITS = 10;
+// LIST: logits of the cells that matter that are kept in LDS; more are read from the row each time.
+constexpr int ROW_THREADS = 1024, LIST = 8192, STEP_BITS = 10, MOST_CHUNKS = MAX_VOCAB / SAMPLE_CHUNK;
 
 struct RowLds {
-    double cell_mass[SAMPLE_CELLS], upto_mass[SAMPLE_CELLS];      // by cell, and with all cells above it
-    uint32_t cell_count[SAMPLE_CELLS], upto_count[SAMPLE_CELLS];
+    double upto_mass[SAMPLE_CELLS + 1];                           // of all cells above
+    uint32_t upto_count[SAMPLE_CELLS + 1];
+    uint32_t low[SAMPLE_CELLS], high[SAMPLE_CELLS];               // least and largest key of a cell that is looked at
+    uint8_t want[SAMPLE_CELLS];
+    double factor[MOST_CHUNKS];                                   // of a chunk's weights
+    int below[MOST_CHUNKS];                                       // its first cell
     uint64_t mass[ROW_THREADS];
     uint32_t count[ROW_THREADS];
-    uint32_t key[ROW_LIST], index[ROW_LIST];                      // of the cell that was looked at last
+    uint32_t key[LIST], index[LIST];
     double wave_mass[16];
-    uint32_t wave_count[16];
+    uint32_t wave_count[16], wave_first[16], wave_last[16];
+    float wave_top[16];
     double found_mass;
-    uint32_t found_count, found_some, n_found, n, lo, hi;
-    int found;
+    uint32_t found_count, found_ties, n, token;
 };
 
-// Inclusive sums over the workgroup's threads, in their order.
-__device__ __forceinline__ uint32_t scan_counts(RowLds &s, uint32_t v) {
-    const int lane = lane_id(), wave = (int)threadIdx.x >> 6;
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t u = (uint32_t)__shfl_up((int)v, d);
-        if (lane >= d) v += u;
-    }
-    if (lane == 63) s.wave_count[wave] = v;
-    __syncthreads();
-    for (int k = 0; k < wave; ++k) v += s.wave_count[k];
-    __syncthreads();
-    return v;
-}
-__device__ __forceinline__ double scan_masses(RowLds &s, double v) {
-    const int lane = lane_id(), wave = (int)threadIdx.x >> 6;
-    v = wave_scan(v);
-    if (lane == 63) s.wave_mass[wave] = v;
-    __syncthreads();
-    double before = 0.0;
-    for (int k = 0; k < wave; ++k) before += s.wave_mass[k];
-    __syncthreads();
-    return before + v;
-}
-// The first thread for which `yes` holds, else the last of those with `some`; -1: none of either.
-__device__ __forceinline__ int first_thread(RowLds &s, bool yes, bool some) {
-    const int tid = (int)threadIdx.x;
-    if (tid == 0) s.found = 0x7FFFFFFF, s.found_some = 0;
-    __syncthreads();
-    const uint64_t a = __ballot(yes), b = __ballot(some);
-    if (lane_id() == 0) {
-        if (a) atomicMin(&s.found, tid + (int)__builtin_ctzll(a));
-        if (b) atomicMax(&s.found_some, (uint32_t)(tid + 64 - __builtin_clzll(b)));
-    }
-    __syncthreads();
-    const int r = s.found != 0x7FFFFFFF ? s.found : (int)s.found_some - 1;
-    __syncthreads();
-    return r;
-}
-
-// A place in the order: a value, what lies above it, how many logits have it, and the weight of one.
+// A place in the order: a value, how many logits have it, the weight of one, and the weight and number of those above.
 struct Place {
-    uint32_t key, ties;
+    uint32_t key, ties, above_count;
     double above, weight;
-    uint32_t above_count;
 };
 
 template <typename L> struct Row {
@@ -197,165 +194,220 @@ template <typename L> struct Row {
     RowLds &s;
     const typename L::T *logits;
     RowHeat h;
-    float top;
-    double top_cell;
-    int listed;          // the cell in s.key and s.index, -1: none; its bounds are in s.lo and s.hi
+    double top_y;
     bool in_list;
 
-    __device__ __forceinline__ double weight(uint32_t key) const { return relative(value_of<L>(key), top, h.inv); }
+    __device__ __forceinline__ double y_of(float x) const { return (double)x * h.cells; }
+    __device__ __forceinline__ double weight(uint32_t key) const { return beside(y_of(value_of<L>(key)), top_y); }
+    __device__ __forceinline__ int cell(float x) const { return cells_below(floor(top_y), floor(y_of(x))); }
 
-    // The keys of cell c, from the last one below the cell above it down to its own lowest: both found by halving.
-    __device__ void bounds(int c) {
-        const int tid = (int)threadIdx.x;
-        if (tid < 2) {
-            // the least key whose logit lies less than c + 1 cells (thread 0) or c cells (thread 1) below the top
-            const int cells = c + 1 - tid;
-            uint32_t lo = Ordered<L>::LOW + 1, hi = key_of_top() + 1;
-            if (cells == SAMPLE_CELLS) hi = lo;
-            while (lo < hi) {
-                const uint32_t mid = lo + (hi - lo) / 2;
-                if (cells_below(top_cell, cell_of(value_of<L>(mid), h)) < cells) hi = mid; else lo = mid + 1;
-            }
-            if (tid == 0) s.lo = lo; else s.hi = lo - 1;
+    // The first cell whose weight with all above it reaches x (or passes it), else the last with logits. In every lane.
+    template <bool PAST> __device__ __forceinline__ int cell_by(double x) const {
+        return first_cell([&](int c) { return PAST ? s.upto_mass[c + 1] > x : s.upto_mass[c + 1] >= x; });
+    }
+    template <typename F> __device__ __forceinline__ int first_cell(F yes) const {
+        int first = SAMPLE_CELLS, last = -1;
+#pragma unroll
+        for (int k = 3; k >= 0; --k) {
+            const int c = lane_id() * 4 + k;
+            const bool some = s.upto_count[c + 1] > s.upto_count[c];
+            if (some && last < 0) last = c;
+            if (some && yes(c)) first = c;
         }
-    }
-    __device__ __forceinline__ uint32_t key_of_top() const { return key_from(top); }
-    static __device__ __forceinline__ uint32_t key_from(float v) {
-        if constexpr (sizeof(typename L::T) == 4)
-            return key_of<L>(v);
-        else
-            return key_of<L>(std::is_same<L, LogitF16>::value ? f2h(v) : f2bf(v));
+        const uint64_t a = __ballot(first < SAMPLE_CELLS), b = __ballot(last >= 0);
+        return a ? __builtin_amdgcn_readlane(first, (int)__builtin_ctzll(a))
+                 : __builtin_amdgcn_readlane(last, 63 - (int)__builtin_clzll(b));
     }
 
-    // Makes cell c the one that is looked at: its bounds, and its logits where they fit.
-    __device__ void look_at(int c) {
-        if (listed == c) return;
-        __syncthreads();
-        bounds(c);
-        if (threadIdx.x == 0) s.n = 0;
-        __syncthreads();
-        listed = c;
-        in_list = s.cell_count[c] <= ROW_LIST;
-        if (!in_list) return;
-        const uint32_t lo = s.lo, hi = s.hi;
-        each_logit([&](uint32_t key, int i) {
-            if (key >= lo && key <= hi) {
-                const uint32_t at = atomicAdd(&s.n, 1u);
-                if (at < ROW_LIST) {
+    // Lists the logits of the cells from `from` to `to` that s.want names, and finds the bounds of each cell's keys.
+    __device__ void gather(int from, int to) {
+        // no logit of these cells lies outside: y's rounding is below the half cell that is added
+        const double most = (floor(top_y) - from + 1.5) / h.cells, least = (floor(top_y) - to - 0.5) / h.cells;
+        const float hi = top_y == __builtin_inf() || from == 0 ? __builtin_inff() : __double2float_ru(most);
+        // (the lowest number, since -infinity is in no cell)
+        const float lo = top_y == __builtin_inf() ? (to ? -3.4028234e38f : __builtin_inff())
+                         : to == SAMPLE_CELLS - 1 ? -3.4028234e38f : fmaxf(__double2float_rd(least), -3.4028234e38f);
+        const int tid = (int)threadIdx.x;
+        constexpr int DEEP = 8;
+        auto test = [&](typename L::T v, int i, bool on) {
+            const float x = L::value(v);
+            on = on && x >= lo && x <= hi;
+            int c = 0;
+            if (on) {
+                c = cell(x);
+                on = s.want[c];
+            }
+            const uint64_t who = __ballot(on);
+            if (!who) return;
+            uint32_t base = 0;
+            const int leader = (int)__builtin_ctzll(who);
+            if (lane_id() == leader) base = atomicAdd(&s.n, (uint32_t)__popcll(who));
+            base = (uint32_t)__builtin_amdgcn_readlane((int)base, leader);
+            if (on) {
+                const uint32_t key = key_of<L>(v), at = base + (uint32_t)__popcll(who & ((1ull << lane_id()) - 1));
+                if (at < LIST) {
                     s.key[at] = key;
                     s.index[at] = (uint32_t)i;
                 }
+                if (key < *(volatile uint32_t *)&s.low[c]) atomicMin(&s.low[c], key);
+                if (key > *(volatile uint32_t *)&s.high[c]) atomicMax(&s.high[c], key);
             }
-        });
-        __syncthreads();
+        };
+        const int whole_steps = p.vocab / (ROW_THREADS * 4);
+        int b = 0;
+        for (; b + DEEP <= whole_steps; b += DEEP) {
+            Four<typename L::T> v[DEEP];
+#pragma unroll
+            for (int k = 0; k < DEEP; ++k) v[k] = *(const Four<typename L::T> *)(logits + ((b + k) * ROW_THREADS + tid) * 4);
+#pragma unroll
+            for (int k = 0; k < DEEP; ++k) {
+                float t = L::value(v[k].v[0]);
+                bool near = t >= lo && t <= hi;
+#pragma unroll
+                for (int e = 1; e < 4; ++e) {
+                    t = L::value(v[k].v[e]);
+                    near |= t >= lo && t <= hi;
+                }
+                if (__any(near))
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) test(v[k].v[e], ((b + k) * ROW_THREADS + tid) * 4 + e, true);
+            }
+        }
+        for (int i0 = b * ROW_THREADS * 4; i0 < p.vocab; i0 += ROW_THREADS) {
+            const int i = i0 + tid;
+            const bool on = i < p.vocab;
+            test(on ? logits[i] : typename L::T(0), i, on);
+        }
     }
 
-    // f(key, index) of every logit of the row.
-    template <typename F> __device__ __forceinline__ void each_logit(F f) const {
-        for (int i = (int)threadIdx.x; i < p.vocab; i += ROW_THREADS) f(key_of<L>(logits[i]), i);
-    }
-    // f(on, key, index) of every logit in the cell that is looked at, whole waves at a time.
-    template <typename F> __device__ __forceinline__ void each(F f) const {
-        const int tid = (int)threadIdx.x, n = in_list ? min((int)s.n, ROW_LIST) : p.vocab;
-        const uint32_t lo = s.lo, hi = s.hi;
-        for (int i0 = 0; i0 < n; i0 += ROW_THREADS) {
-            const int i = i0 + tid;
-            const bool some = i < n;
-            uint32_t key = 0, at = (uint32_t)i;
-            if (some) {
-                key = in_list ? s.key[i] : key_of<L>(logits[i]);
-                if (in_list) at = s.index[i];
-            }
-            f(some && key >= lo && key <= hi, key, at);
+    // f(key, index) of every logit whose key is from lo to hi, in cells that were gathered.
+    template <typename F> __device__ __forceinline__ void each(uint32_t lo, uint32_t hi, F f) const {
+        const int tid = (int)threadIdx.x, n = in_list ? (int)s.n : p.vocab;
+        for (int i = tid; i < n; i += ROW_THREADS) {
+            const uint32_t key = in_list ? s.key[i] : key_of<L>(logits[i]);
+            if (key >= lo && key <= hi) f(key, in_list ? s.index[i] : (uint32_t)i);
         }
+    }
+
+    // Sums over the threads before each one, the first thread for which `yes` holds of the sums up to it (else the last with a
+    // count), and what lies before that one.
+    template <typename F> __device__ __forceinline__ int first_step(uint32_t n, double m, F yes) {
+        const int tid = (int)threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
+        uint32_t upto_n = n;
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t u = (uint32_t)__shfl_up((int)upto_n, d);
+            if (lane >= d) upto_n += u;
+        }
+        double upto_m = wave_scan(m);
+        if (lane == 63) {
+            s.wave_count[wave] = upto_n;
+            s.wave_mass[wave] = upto_m;
+        }
+        __syncthreads();
+        uint32_t before_n = 0;
+        double before_m = 0.0;
+        for (int k = 0; k < wave; ++k) {
+            before_n += s.wave_count[k];
+            before_m += s.wave_mass[k];
+        }
+        upto_n += before_n;
+        upto_m += before_m;
+        const uint64_t a = __ballot(n && yes(upto_n, upto_m)), b = __ballot(n > 0);
+        if (lane == 0) {
+            s.wave_first[wave] = a ? (uint32_t)(wave * 64 + (int)__builtin_ctzll(a)) : ROW_THREADS;
+            s.wave_last[wave] = b ? (uint32_t)(wave * 64 + 64 - (int)__builtin_clzll(b)) : 0;
+        }
+        __syncthreads();
+        const uint32_t f = s.wave_first[lane & 15], l = s.wave_last[lane & 15];
+        const uint64_t c = __ballot(f < ROW_THREADS) & 0xFFFF, d = __ballot(l > 0) & 0xFFFF;
+        int t = 0;
+        if (c) t = __builtin_amdgcn_readlane((int)f, (int)__builtin_ctzll(c));
+        else if (d) t = __builtin_amdgcn_readlane((int)l, 63 - (int)__builtin_clzll(d)) - 1;
+        if (tid == t) {
+            s.found_count = upto_n - n;
+            s.found_mass = upto_m - m;
+            s.found_ties = n;
+        }
+        __syncthreads();
+        return t;
     }
 
     // The value of cell c at which the running count (BY_COUNT) or weight reaches `goal` (or passes it: PAST).
     template <bool BY_COUNT, bool PAST> __device__ Place find(int c, double goal) {
-        look_at(c);
         const int tid = (int)threadIdx.x;
+        uint32_t lo = s.low[c], hi = s.high[c];
         Place r;
-        r.above = c ? s.upto_mass[c - 1] : 0.0;
-        r.above_count = c ? s.upto_count[c - 1] : 0;
-        uint32_t lo = s.lo, hi = s.hi;
+        r.above = s.upto_mass[c];
+        r.above_count = s.upto_count[c];
+        r.ties = s.upto_count[c + 1] - r.above_count;
         // weights of this cell are below 2^(1/8 - c/8) of the largest
-        const int n_bits = 32 - __builtin_clz(max(s.cell_count[c], 1u)), shift = c / 8 + 61 - n_bits;
+        const int n_bits = 32 - __builtin_clz(max(r.ties, 1u)), shift = c / 8 + 61 - n_bits;
         const double unit = power2(-shift);
-        for (;;) {
-            const int cut = max(0, 32 - (hi == lo ? 32 : __builtin_clz(hi - lo)) - STEP_BITS);
+        while (hi > lo) {
+            const int cut = max(0, 32 - __builtin_clz(hi - lo) - STEP_BITS);
             s.mass[tid] = 0;
             s.count[tid] = 0;
             __syncthreads();
-            each([&](bool on, uint32_t key, uint32_t) {
-                on = on && key >= lo && key <= hi;
-                const uint64_t w = on ? whole(weight(key), shift) : 0;
-                add_to(s.mass, s.count, on ? (int)((hi - key) >> cut) : 0, w, on);
+            each(lo, hi, [&](uint32_t key, uint32_t) {
+                add_to(s.mass, s.count, (int)((hi - key) >> cut), whole(weight(key), shift), true);
             });
             __syncthreads();
-            const uint32_t n = s.count[tid];
-            const double m = (double)s.mass[tid] * unit;
-            const uint32_t upto_n = scan_counts(s, n);
-            const double upto_m = scan_masses(s, m);
-            const bool yes = n && (BY_COUNT ? (double)(r.above_count + upto_n) >= goal
-                                            : PAST ? r.above + upto_m > goal : r.above + upto_m >= goal);
-            const int t = max(first_thread(s, yes, n > 0), 0);
-            if (tid == t) {
-                s.found_count = upto_n - n;
-                s.found_mass = upto_m - m;
-                s.n_found = n;
-            }
-            __syncthreads();
+            const int t = first_step(s.count[tid], (double)s.mass[tid] * unit, [&](uint32_t n, double m) {
+                return BY_COUNT ? (double)(r.above_count + n) >= goal : PAST ? r.above + m > goal : r.above + m >= goal;
+            });
             r.above += s.found_mass;
             r.above_count += s.found_count;
-            r.ties = s.n_found;
+            r.ties = s.found_ties;
             hi -= (uint32_t)t << cut;
             lo = max(lo, hi - ((1u << cut) - 1u));
-            __syncthreads();
-            if (cut == 0) break;
         }
         r.key = hi;
         r.weight = weight(hi);
         return r;
     }
 
-    // The index of the t-th (from 0) of the logits whose key is `key`, in the cell that is looked at.
-    __device__ int nth_index(uint32_t key, uint32_t t) {
+    // The index of the t-th (from 0) of the logits whose key is `key`, of which there are `ties`.
+    __device__ uint32_t nth_index(uint32_t key, uint32_t t, uint32_t ties) {
         const int tid = (int)threadIdx.x;
+        if (ties == 1) {
+            each(key, key, [&](uint32_t, uint32_t at) { s.token = at; });
+            __syncthreads();
+            return s.token;
+        }
         uint32_t lo = 0, hi = (uint32_t)p.vocab - 1;
-        for (;;) {
-            const int cut = max(0, 32 - (hi == lo ? 32 : __builtin_clz(hi - lo)) - STEP_BITS);
-            s.mass[tid] = 0;
+        while (hi > lo) {
+            const int cut = max(0, 32 - __builtin_clz(hi - lo) - STEP_BITS);
             s.count[tid] = 0;
             __syncthreads();
-            each([&](bool on, uint32_t k, uint32_t at) {
-                on = on && k == key && at >= lo && at <= hi;
-                add_to(s.mass, s.count, on ? (int)((at - lo) >> cut) : 0, 0, on);
+            each(key, key, [&](uint32_t, uint32_t at) {
+                if (at >= lo && at <= hi) atomicAdd(&s.count[(at - lo) >> cut], 1u);
             });
             __syncthreads();
-            const uint32_t n = s.count[tid], upto = scan_counts(s, n);
-            const int f = max(first_thread(s, upto > t, n > 0), 0);
-            if (tid == f) s.found_count = upto - n;
-            __syncthreads();
+            const int f = first_step(s.count[tid], 0.0, [&](uint32_t n, double) { return n > t; });
             t -= min(t, s.found_count);
             lo += (uint32_t)f << cut;
             hi = min(hi, lo + ((1u << cut) - 1u));
-            __syncthreads();
-            if (cut == 0) break;
         }
-        return (int)lo;
+        return lo;
     }
 };
 
 template <typename L> __global__ void __launch_bounds__(ROW_THREADS) moe_sample_row_kernel(SampleParams p) {
     __shared__ RowLds s;
-    const int row = (int)blockIdx.x, tid = (int)threadIdx.x, group = tid >> 8, cell = tid & 255;
-    fill_exp_table();
+    const int row = (int)blockIdx.x, tid = (int)threadIdx.x, lane = lane_id(), group = tid >> 8, cell = tid & 255;
     const RowHeat h = row_heat(p, row);
-    const SampleHead *head = p.head + (int64_t)row * p.chunks;
-    // the largest logit (at most 256 chunks: a lane has up to 4 of them), the same in every wave
-    float top = -__builtin_inff();
-    for (int c = lane_id(); c < p.chunks; c += 64) top = fmaxf(top, head[c].top);
-    top = wave_max(top);
+    SampleHead head = {0.0, -__builtin_inff(), 0};
+    if (tid < p.chunks) head = p.head[(int64_t)row * p.chunks + tid];
+    if (tid < SAMPLE_CELLS) {
+        s.want[tid] = 0;
+        s.low[tid] = 0xFFFFFFFFu;
+        s.high[tid] = 0;
+    }
+    if (tid == 0) s.n = 0;
+    float top = wave_max(head.top);
+    if (lane == 0) s.wave_top[tid >> 6] = top;
+    fill_exp_table();
+    top = wave_max(s.wave_top[lane & 15]);
     if (!(top > -__builtin_inff())) {
         if (tid == 0) {
             raise_flag(p.flags, MOE_FLAG_LOGITS);
@@ -364,100 +416,161 @@ template <typename L> __global__ void __launch_bounds__(ROW_THREADS) moe_sample_
         }
         return;
     }
-    const double top_cell = cell_of(top, h);
-    // the chunks' cells on the row's: thread (group, cell) takes every fourth chunk
+    const double top_y = (double)top * h.cells;
+    if (tid < p.chunks) {
+        const bool some = head.top > -__builtin_inff();
+        s.below[tid] = some ? cells_below(floor(top_y), floor(head.top_y)) : -1;
+        s.factor[tid] = some ? beside(head.top_y, top_y) * power2(-50) : 0.0;
+    }
+    __syncthreads();
+    // the chunks' cells on the row's: thread (group, cell) takes every fourth chunk; what goes into the last cell from
+    // elsewhere is added by all threads
     double m = 0.0, tail = 0.0;
     uint32_t n = 0, tail_n = 0;
+    const int64_t base = (int64_t)row * p.chunks * SAMPLE_CELLS;
+#pragma unroll 8
     for (int c = group; c < p.chunks; c += 4) {
-        const SampleHead hd = head[c];
-        if (!(hd.top > -__builtin_inff())) continue;
-        const int off = cells_below(top_cell, hd.cell);
-        const double f = relative(hd.top, top, h.inv) * power2(-50);
-        const int64_t at = ((int64_t)row * p.chunks + c) * SAMPLE_CELLS;
-        if (cell < SAMPLE_CELLS - 1 && cell >= off) {
-            m += (double)p.mass[at + cell - off] * f;
-            n += p.count[at + cell - off];
+        const int off = s.below[c], from = cell - off;
+        const bool here = off >= 0 && from >= 0;
+        const int64_t at = base + (int64_t)c * SAMPLE_CELLS + (here ? from : 0);
+        const uint64_t w = p.mass[at];
+        const uint32_t k = p.count[at];
+        if (here && cell < SAMPLE_CELLS - 1) {
+            m += (double)w * s.factor[c];
+            n += k;
         }
-        if (cell + off >= SAMPLE_CELLS - 1) {
-            tail += (double)p.mass[at + cell] * f;
-            tail_n += p.count[at + cell];
+        if (off >= 0 && cell + off >= SAMPLE_CELLS - 1) {
+            tail += (double)p.mass[base + (int64_t)c * SAMPLE_CELLS + cell] * s.factor[c];
+            tail_n += p.count[base + (int64_t)c * SAMPLE_CELLS + cell];
         }
     }
-    // what goes into the last cell, from all threads
-    tail = scan_masses(s, tail);
-    tail_n = scan_counts(s, tail_n);
-    if (tid == ROW_THREADS - 1) { s.found_mass = tail; s.found_count = tail_n; }
     s.count[tid] = n;
     ((double *)s.mass)[tid] = m;
+    tail = wave_sum(tail);
+    for (int d = 32; d; d >>= 1) tail_n += (uint32_t)__shfl_xor((int)tail_n, d);
+    if (lane == 0) {
+        s.wave_mass[tid >> 6] = tail;
+        s.wave_count[tid >> 6] = tail_n;
+    }
     __syncthreads();
-    if (group == 0) {
-        for (int k = 1; k < 4; ++k) {
-            n += s.count[tid + 256 * k];
-            m += ((double *)s.mass)[tid + 256 * k];
+    if (tid < 64) {
+        double w[4], sum = 0.0;
+        uint32_t k[4], sum_n = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int c = tid * 4 + e;
+            w[e] = 0.0;
+            k[e] = 0;
+            for (int g = 0; g < 4; ++g) {
+                w[e] += ((double *)s.mass)[g * 256 + c];
+                k[e] += s.count[g * 256 + c];
+            }
+            if (c == SAMPLE_CELLS - 1)
+                for (int g = 0; g < 16; ++g) {
+                    w[e] += s.wave_mass[g];
+                    k[e] += s.wave_count[g];
+                }
+            sum += w[e];
+            sum_n += k[e];
         }
-        if (cell == SAMPLE_CELLS - 1) { n = s.found_count; m = s.found_mass; }
-    } else {
-        n = 0;
-        m = 0.0;
-    }
-    const uint32_t upto_n = scan_counts(s, n);
-    const double upto_m = scan_masses(s, m);
-    if (group == 0) {
-        s.cell_mass[cell] = m;
-        s.cell_count[cell] = n;
-        s.upto_mass[cell] = upto_m;
-        s.upto_count[cell] = upto_n;
+        double before = wave_scan(sum) - sum;
+        uint32_t upto = sum_n;
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t u = (uint32_t)__shfl_up((int)upto, d);
+            if (tid >= d) upto += u;
+        }
+        uint32_t before_n = upto - sum_n;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s.upto_mass[tid * 4 + e] = before;
+            s.upto_count[tid * 4 + e] = before_n;
+            before += w[e];
+            before_n += k[e];
+        }
+        if (tid == 63) {
+            s.upto_mass[SAMPLE_CELLS] = before;
+            s.upto_count[SAMPLE_CELLS] = before_n;
+        }
     }
     __syncthreads();
-    const uint32_t all_n = s.upto_count[SAMPLE_CELLS - 1];
-    const double all = s.upto_mass[SAMPLE_CELLS - 1];
+    const double all = s.upto_mass[SAMPLE_CELLS];
+    Row<L> r = {p, s, row_of<L>(p, row), h, top_y, true};
 
-    Row<L> r = {p, s, row_of<L>(p, row), h, top, top_cell, -1, false};
-    // the first cell that reaches a count or a weight
-    auto cell_by = [&](bool yes) { return max(first_thread(s, group == 0 && n && yes, group == 0 && n), 0); };
-    double kept = all;
+    // the cells that the cuts and the draw fall into: of top-p and the draw a first and a last one, since what the cuts before
+    // them leave is known to a cell only
     const uint32_t k = h.greedy ? 1u : p.top_k && p.top_k[row] > 0 ? (uint32_t)p.top_k[row] : 0xFFFFFFFFu;
-    if (k < all_n) {
-        const Place at = r.template find<true, false>(cell_by(upto_n >= k), (double)k);
+    const float top_p = p.top_p ? p.top_p[row] : 1.0f, asked = p.min_p ? p.min_p[row] : 0.0f;
+    const float min_p = asked > 1.0f ? 1.0f : asked, given = p.u[row];
+    const double u = (double)(given > 0.0f ? fminf(given, 0.99999994f) : 0.0f);
+    const bool by_k = k < s.upto_count[SAMPLE_CELLS], by_p = !h.greedy && top_p < 1.0f, by_m = !h.greedy && min_p > 0.0f;
+    const int k_cell = by_k ? r.first_cell([&](int c) { return s.upto_count[c + 1] >= k; }) : 0;
+    double least = all, most = all;
+    if (by_k) least = s.upto_mass[k_cell], most = s.upto_mass[k_cell + 1];
+    int p_from = 0, p_to = -1, m_cell = 0;
+    if (by_p) {
+        p_from = r.template cell_by<false>((double)top_p * least);
+        p_to = r.template cell_by<false>((double)top_p * most);
+        least = fmin(least, s.upto_mass[p_from]);
+        most = fmin(most, s.upto_mass[p_to + 1]);
+    }
+    double floor_y = 0.0;
+    if (by_m) {
+        // the cell that the least weight lies in
+        floor_y = top_y == __builtin_inf() ? top_y : top_y + 8.0 * log2((double)min_p);
+        m_cell = cells_below(floor(top_y), floor(floor_y));
+        least = fmin(least, s.upto_mass[m_cell]);
+        most = fmin(most, s.upto_mass[m_cell + 1]);
+    }
+    const int d_from = r.template cell_by<true>(u * least), d_to = r.template cell_by<true>(u * most);
+    int from = d_from, to = d_to;
+    if (by_k) from = min(from, k_cell), to = max(to, k_cell);
+    if (by_p) from = min(from, p_from), to = max(to, p_to);
+    if (by_m) from = min(from, m_cell), to = max(to, m_cell);
+    if (tid < SAMPLE_CELLS)
+        s.want[tid] = (tid >= d_from && tid <= d_to) || (by_k && tid == k_cell) || (by_p && tid >= p_from && tid <= p_to) ||
+                      (by_m && tid == m_cell);
+    __syncthreads();
+    r.gather(from, to);
+    __syncthreads();
+    r.in_list = s.n <= LIST;
+
+    double kept = all;
+    if (by_k) {
+        const Place at = r.template find<true, false>(k_cell, (double)k);
         kept = at.above + (double)(k - at.above_count) * at.weight;
     }
-    const double first_k = kept;
-    const float top_p = p.top_p ? p.top_p[row] : 1.0f, asked = p.min_p ? p.min_p[row] : 0.0f;
-    const float min_p = asked > 1.0f ? 1.0f : asked;
-    if (!h.greedy && top_p < 1.0f) {
-        const double goal = (double)top_p * first_k;
-        const Place at = r.template find<false, false>(cell_by(upto_m >= goal), goal);
+    if (by_p) {
+        const double goal = (double)top_p * kept;
+        const Place at = r.template find<false, false>(min(max(r.template cell_by<false>(goal), p_from), p_to), goal);
         const double ties = at.weight > 0.0 ? ceil((goal - at.above) / at.weight) : 1.0;
         kept = fmin(kept, at.above + fmin(fmax(ties, 1.0), (double)at.ties) * at.weight);
     }
-    if (!h.greedy && min_p > 0.0f) {
-        // the cell that the least weight lies in, and the part of it that is not below that
-        const double least = top == __builtin_inff() ? (double)top : (double)top + log((double)min_p) / h.inv;
-        const int c = cells_below(top_cell, floor(least * h.cells));
-        r.look_at(c);
-        const int n_bits = 32 - __builtin_clz(max(s.cell_count[c], 1u)), shift = c / 8 + 61 - n_bits;
+    if (by_m) {
+        // the part of its cell that is not below the least weight
+        const uint32_t count = s.upto_count[m_cell + 1] - s.upto_count[m_cell];
+        const int n_bits = 32 - __builtin_clz(max(count, 1u)), shift = m_cell / 8 + 61 - n_bits;
         if (tid == 0) s.mass[0] = 0;
         __syncthreads();
         uint64_t sum = 0;
-        r.each([&](bool on, uint32_t key, uint32_t) {
-            const double w = on ? r.weight(key) : 0.0;
-            if (on && w >= (double)min_p) sum += whole(w, shift);
-        });
+        if (count)
+            r.each(s.low[m_cell], s.high[m_cell], [&](uint32_t key, uint32_t) {
+                const double w = r.weight(key);
+                if (w >= (double)min_p) sum += whole(w, shift);
+            });
         for (int d = 32; d; d >>= 1) sum += (uint64_t)__shfl_xor((long long)sum, d);
-        if (lane_id() == 0) atomicAdd((unsigned long long *)s.mass, (unsigned long long)sum);
+        if (lane == 0 && sum) atomicAdd((unsigned long long *)s.mass, (unsigned long long)sum);
         __syncthreads();
-        kept = fmin(kept, (c ? s.upto_mass[c - 1] : 0.0) + (double)s.mass[0] * power2(-shift));
+        kept = fmin(kept, s.upto_mass[m_cell] + (double)s.mass[0] * power2(-shift));
         __syncthreads();
     }
-    const float u = p.u[row];
-    const double goal = (double)(u > 0.0f ? fminf(u, 0.99999994f) : 0.0f) * kept;
-    const Place at = r.template find<false, true>(cell_by(upto_m > goal), goal);
+    const double goal = u * kept;
+    const Place at = r.template find<false, true>(min(max(r.template cell_by<true>(goal), d_from), d_to), goal);
     const double t = at.weight > 0.0 ? floor((goal - at.above) / at.weight) : 0.0;
-    const int token = r.nth_index(at.key, (uint32_t)fmin(fmax(t, 0.0), (double)(at.ties - 1)));
+    const uint32_t token = r.nth_index(at.key, (uint32_t)fmin(fmax(t, 0.0), (double)(at.ties - 1)), at.ties);
     if (tid == 0) {
-        const float x = value_of<L>(at.key);
-        p.tokens[row] = token;
-        p.logprobs[row] = h.greedy ? 0.0f : (float)((x == top ? 0.0 : ((double)x - (double)top) * h.inv) - log(all));
+        const double y = r.y_of(value_of<L>(at.key));
+        p.tokens[row] = (int32_t)token;
+        p.logprobs[row] = h.greedy ? 0.0f : (float)((y == top_y ? 0.0 : (y - top_y) * 0.08664339756999316) - log(all));
     }
 }
 
