@@ -171,13 +171,13 @@ struct VerifyParams {
                                 // copied and stored whole
 };
 
-// Sampling (sample_kernels.hip). Logits of a row are taken in chunks; of each a histogram over cells of an eighth of an octave of
+// Sampling (sample_kernels.hip). Logits of a row are taken in chunks; of each a histogram over cells of a quarter of an octave of
 // their weight, the same grid for all chunks of a row.
 constexpr int SAMPLE_CHUNK = 4096, SAMPLE_CELLS = 256;
 struct SampleHead {
-    double top_y;               // the largest logit, in cells
+    double top_g;               // the largest logit's place on the grid
     float top;                  // -infinity: nothing above that
-    uint32_t pad;
+    uint32_t listed;            // whether the chunk's logits are listed
 };
 struct SampleParams {
     const void *logits;
@@ -191,6 +191,8 @@ struct SampleParams {
     SampleHead *head;           // [rows][chunks]
     uint64_t *mass;             // [rows][chunks][SAMPLE_CELLS], in 2^-50 of the chunk's largest weight
     uint16_t *count;            // [rows][chunks][SAMPLE_CELLS]
+    uint16_t *start;            // [rows][chunks][SAMPLE_CELLS]: where a cell's logits begin in
+    uint16_t *list;             // [rows][chunks][SAMPLE_CHUNK]: their numbers within the chunk
 };
 
 struct KeepParams {

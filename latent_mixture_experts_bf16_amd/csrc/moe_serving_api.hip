@@ -238,13 +238,17 @@ static int64_t sample_layout(int64_t rows, int64_t vocab, char *base, SamplePara
     const int64_t chunks = (vocab + SAMPLE_CHUNK - 1) / SAMPLE_CHUNK;
     const int64_t mass = rows * chunks * (int64_t)sizeof(SampleHead);
     const int64_t count = mass + rows * chunks * SAMPLE_CELLS * 8;
+    const int64_t start = count + rows * chunks * SAMPLE_CELLS * 2;
+    const int64_t list = start + rows * chunks * SAMPLE_CELLS * 2;
     if (p) {
         p->chunks = (int32_t)chunks;
         p->head = (SampleHead *)base;
         p->mass = (uint64_t *)(base + mass);
         p->count = (uint16_t *)(base + count);
+        p->start = (uint16_t *)(base + start);
+        p->list = (uint16_t *)(base + list);
     }
-    return count + rows * chunks * SAMPLE_CELLS * 2;
+    return list + rows * chunks * SAMPLE_CHUNK * 2;
 }
 
 extern "C" int64_t moe_sample_workspace(int32_t rows, int32_t vocab) {

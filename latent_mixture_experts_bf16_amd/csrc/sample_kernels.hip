@@ -2,7 +2,7 @@
 //
 // All three cuts, and the draw, are places in one order: falling logits, equal ones by index. None of them needs the row
 // sorted, only the running count or weight at a few places. So the logits of a row are counted, and their weights summed, over
-// the cells of a grid of an eighth of an octave of weight (a workgroup per chunk, whole card), and one workgroup per
+// the cells of a grid of a quarter of an octave of weight (a workgroup per chunk, whole card), and one workgroup per
 // row finds the cells that matter and looks at their logits alone, narrowing to one value in steps of 10 bits of its
 // ordered bits. Whole tokens come out, so weights and sums are in 64 bits. Where atomics add in an order that varies, they add
 // whole numbers (the weight in 2^-50 of the largest one), so that the same inputs always give the same token.
@@ -44,34 +44,39 @@ template <typename L> __device__ __forceinline__ float value_of(uint32_t key) {
     return O::value(key & O::SIGN ? key & ~O::SIGN : ~key & MASK);
 }
 
-// Temperature of a row as cells (eighths of an octave of weight) of a logit, and whether only the largest logit counts. A greedy
-// row is one that keeps the first token of the order; its weights are then of no matter. (An infinite T counts as the
+// Temperature of a row, as 32nds of an octave of weight for each unit of a logit, and whether only the largest logit counts. A
+// greedy row is one that keeps the first token of the order; its weights are then of no matter. (An infinite T counts as the
 // largest finite one, so that a logit of -infinity still weighs nothing.)
 struct RowHeat {
-    double cells;
+    double steps;
     bool greedy;
 };
 __device__ __forceinline__ RowHeat row_heat(const SampleParams &p, int row) {
     const float T = p.temperature ? p.temperature[row] : 1.0f;
     const bool greedy = !(T > 0.0f);
-    return {(greedy ? 1.0 : 1.0 / (double)fminf(T, 3.4028234e38f)) * (8.0 * 1.4426950408889634), greedy};
+    return {(greedy ? 1.0 : 1.0 / (double)fminf(T, 3.4028234e38f)) * (32.0 * 1.4426950408889634), greedy};
 }
-// How many cells below the one of the largest a cell is, 0 .. SAMPLE_CELLS - 1 (the last one holds all that lie further down).
-__device__ __forceinline__ int cells_below(double top, double cell) {
-    const double d = top == cell ? 0.0 : top - cell;
+
+// The grid that all logits of a row are placed on: the nearest whole number of steps, rising with the logit, the same wherever
+// it is computed. Eight steps make a cell. (1.5 2^52 added leaves the number in the low bits; from 2^50 on there are only
+// whole numbers.)
+constexpr double ROUND = 6755399441055744.0;
+__device__ __forceinline__ double grid(float x, double steps) {
+    const double near = fma((double)x, steps, ROUND) - ROUND, far = (double)x * steps;
+    return fabs(far) < 0x1p50 ? near : far;
+}
+// How many cells below the one of the largest, 0 .. SAMPLE_CELLS - 1 (the last one holds all that lie further down: nearly 64
+// octaves, where weights are nothing in 2^-50).
+__device__ __forceinline__ int cells_below(double top, double g) {
+    const double d = top == g ? 0.0 : floor(top * 0.125) - floor(g * 0.125);
     return d < (double)(SAMPLE_CELLS - 1) ? (int)d : SAMPLE_CELLS - 1;
 }
 
-// 2^(y / 8) for y <= 0, to about 2^-48: y = n / 4 + r with |r| <= 1/8, 2^(n / 32) from a table (its entries lie on different
-// banks of LDS) and the exponent, times the Taylor polynomial of degree 5 of e^(r log(2) / 8) (its remainder is below
-// 3e-15 of the value where r is largest). n is rounded by adding 1.5 2^52, which leaves it in the low bits. Below 2^-64, where
-// nothing is left of it in what follows, 2^-64.
-__device__ __forceinline__ double weight_of(double y) {
-    constexpr double ROUND = 6755399441055744.0, C = 0.08664339756999316;     // log(2) / 8
-    y = fmax(y, -512.0);
-    const double t = fma(y, 4.0, ROUND);
-    const double r = fma(t - ROUND, -0.25, y);
-    const int k = (int)(uint32_t)(uint64_t)__double_as_longlong(t);
+// 2^((k + r) / 32) for a whole k <= 0 and |r| <= 1/2, to about 2^-48: 2^(k / 32) from a table (its entries lie on different
+// banks of LDS) and the exponent, times the Taylor polynomial of degree 5 of e^(r log(2) / 32), whose remainder is below
+// 3e-15 of the value where r is largest.
+__device__ __forceinline__ double power32(int k, double r) {
+    constexpr double C = 0.02166084939249829;     // log(2) / 32
     const double m = exp_table()[k & 31];
     double e = fma(r, C * C * C * C * C / 120.0, C * C * C * C / 24.0);
     e = fma(e, r, C * C * C / 6.0);
@@ -81,11 +86,17 @@ __device__ __forceinline__ double weight_of(double y) {
     const uint64_t bits = (uint64_t)__double_as_longlong(e) + ((uint64_t)(uint32_t)((k >> 5) * (1 << 20)) << 32);
     return __longlong_as_double((long long)bits);
 }
-// The weight of a logit beside the largest, y and top_y in cells. Where the largest is infinite, all weight is on it.
-__device__ __forceinline__ double beside(double y, double top_y) {
-    return y == top_y ? 1.0 : top_y == __builtin_inf() ? 0.0 : weight_of(y - top_y);
+// Weights are in 2^(top / 32), top being the largest logit's place on the grid. Where that is infinite, all weight is
+// on it. What lies 64 octaves below weighs nothing.
+__device__ __forceinline__ double weight_of(float x, double steps, double top) {
+    if (top == __builtin_inf()) return x == __builtin_inff() ? 1.0 : 0.0;
+    const double g = grid(x, steps), d = g - top;
+    if (!(d > -2048.0)) return 0.0;
+    return power32((int)d, fabs(g) < 0x1p50 ? fma((double)x, steps, -g) : 0.0);
 }
-// A weight of at most 1 as a whole number of 2^-50, to nearest: the low bits of its sum with 4.
+// 2^(d / 32) of whole numbers d <= 0.
+__device__ __forceinline__ double power32_of(double d) { return d >= -2048.0 ? power32((int)d, 0.0) : 0.0; }
+// A weight of at most 2 as a whole number of 2^-50, to nearest: the low bits of its sum with 4.
 __device__ __forceinline__ uint64_t whole50(double w) {
     return (uint64_t)__double_as_longlong(fma(w, 0x1p50, 0x1p52)) & 0xFFFFFFFFFFFFFull;
 }
@@ -97,36 +108,45 @@ template <typename L> __device__ __forceinline__ const typename L::T *row_of(con
     return (const typename L::T *)p.logits + (int64_t)row * p.stride;
 }
 
-// Add to a cell of a histogram in LDS. Where the lanes that do all have the same one (rows of equal logits), once for all.
-__device__ __forceinline__ void add_to(uint64_t *mass, uint32_t *count, int at, uint64_t w, bool on) {
-    if (!on) return;
-    if (__all(at == uniform(at))) {
-        const uint64_t who = __ballot(true);
-        if (__popcll(who) == 64) {
-            for (int d = 32; d; d >>= 1) w += (uint64_t)__shfl_xor((long long)w, d);
-            if (lane_id() == 0) {
-                atomicAdd((unsigned long long *)mass + at, (unsigned long long)w);
-                atomicAdd(count + at, 64u);
-            }
-            return;
-        }
-    }
-    atomicAdd((unsigned long long *)mass + at, (unsigned long long)w);
-    atomicAdd(count + at, 1u);
+// Inclusive sums of counts along the lanes.
+__device__ __forceinline__ uint32_t wave_count_scan(uint32_t v) {
+#define MOE_ADD_STEP(CTRL, ROWS) v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false)
+    MOE_ADD_STEP(0x111, 0xF);
+    MOE_ADD_STEP(0x112, 0xF);
+    MOE_ADD_STEP(0x114, 0xF);
+    MOE_ADD_STEP(0x118, 0xF);
+    MOE_ADD_STEP(0x142, 0xA);
+    MOE_ADD_STEP(0x143, 0xC);
+#undef MOE_ADD_STEP
+    return v;
 }
 
-// ------------------------------------------------------------------ the histogram of a chunk
+// Add a logit's weight to a cell of a histogram in LDS: where all lanes have the same logit, once for all.
+__device__ __forceinline__ void add_to(uint64_t *mass, uint32_t *count, int at, uint64_t w, float x) {
+    const uint64_t on = __ballot(true);
+    const bool same = __ballot(__float_as_int(x) == uniform(__float_as_int(x))) == on;
+    const uint32_t n = same ? (uint32_t)__popcll(on) : 1u;
+    if (!same || lane_id() == (int)__builtin_ctzll(on)) {
+        atomicAdd((unsigned long long *)mass + at, (unsigned long long)(w * n));
+        atomicAdd(count + at, n);
+    }
+}
 
+// ------------------------------------------------------------------ the cells of a chunk
+
+// Besides counts and weights, the chunk's logits but those of its last cell are listed by cell (their numbers within the chunk), so that
+// the row's workgroup reads only those of the cells that matter: a pass over the row by one workgroup takes 11 us and more.
 template <typename L> __global__ void __launch_bounds__(256) moe_sample_cells_kernel(SampleParams p) {
     __shared__ uint64_t mass[SAMPLE_CELLS];
     __shared__ uint32_t count[SAMPLE_CELLS];
+    __shared__ __align__(16) uint16_t list[SAMPLE_CHUNK];
+    __shared__ uint16_t start[SAMPLE_CELLS];
     __shared__ float tops[4];
-    const int row = (int)(blockIdx.z * gridDim.y + blockIdx.y), tid = (int)threadIdx.x, wave = tid >> 6;
+    const int row = (int)(blockIdx.z * gridDim.y + blockIdx.y), tid = (int)threadIdx.x, wave = tid >> 6, lane = lane_id();
     if (row >= p.rows) return;
     const int c = (int)blockIdx.x;
     float x[SHARE];
-    const int part = c * (SAMPLE_CHUNK / VOCAB_CHUNK) + wave;
-    load_share<L>(row_of<L>(p, row), part, p.vocab, -__builtin_inff(), x);
+    load_share<L>(row_of<L>(p, row), c * (SAMPLE_CHUNK / VOCAB_CHUNK) + wave, p.vocab, -__builtin_inff(), x);
     mass[tid] = 0;
     count[tid] = 0;
     fill_exp_table();
@@ -135,53 +155,94 @@ template <typename L> __global__ void __launch_bounds__(256) moe_sample_cells_ke
 #pragma unroll
     for (int k = 0; k < SHARE; ++k) top = fmaxf(top, x[k]);      // not a NaN: the other operand
     top = wave_max(top);
-    if (lane_id() == 0) tops[wave] = top;
+    if (lane == 0) tops[wave] = top;
     __syncthreads();
     top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
     const int64_t at = (int64_t)row * p.chunks + c;
-    const double top_y = (double)top * h.cells, cell = floor(top_y);
-    if (tid == 0) p.head[at] = {top_y, top, 0};
+    const double top_g = grid(top, h.steps);
+    // Two kinds of chunks are taken slowly, and not listed: with an infinite logit, or a temperature next to 0 (places that 32 bits
+    // do not hold); with many equal logits (a wave's first ones), whose additions at one place would take one after another
+    const float lowest = (float)((top_g - 2048.0) / h.steps);      // what lies below weighs nothing
+    const bool equal = x[0] > lowest && __ballot(x[0] == __int_as_float(uniform(__float_as_int(x[0])))) == ~0ull;
+    const bool slow = __syncthreads_or(equal || !(fabs(top_g) < 0x1p29)) != 0;
+    if (tid == 0) p.head[at] = {top_g, top, !slow};
     if (!(top > -__builtin_inff())) return;
-    if (top < __builtin_inff()) {
-#pragma unroll
-        for (int k = 0; k < SHARE; ++k) {
-            const double y = (double)x[k] * h.cells;
-            const double d = fmin(cell - floor(y), (double)(SAMPLE_CELLS - 1));
-            add_to(mass, count, (int)d, whole50(weight_of(y - top_y)), x[k] > -__builtin_inff());     // a NaN is not
+    if (slow) {
+#pragma unroll 1
+        for (int i = c * SAMPLE_CHUNK + tid; i < min(p.vocab, (c + 1) * SAMPLE_CHUNK); i += 256) {
+            const float v = L::value(row_of<L>(p, row)[i]);
+            if (v > -__builtin_inff())
+                add_to(mass, count, cells_below(top_g, grid(v, h.steps)), whole50(weight_of(v, h.steps, top_g)), v);
         }
-    } else {
+        __syncthreads();
+        p.mass[at * SAMPLE_CELLS + tid] = mass[tid];
+        p.count[at * SAMPLE_CELLS + tid] = (uint16_t)count[tid];
+        return;
+    }
+    // Cell and number within it; a logit in the last cell has none. Places on the grid are 32-bit whole numbers.
+    // What lies far below, or is a NaN, is taken to 2048 steps below the top, where it weighs nothing.
+    uint32_t place[SHARE], last_n = 0;
+    uint64_t last_w = 0;
+    const int top_n = (int)top_g;
 #pragma unroll
-        for (int k = 0; k < SHARE; ++k) {
-            const bool on = x[k] > -__builtin_inff(), is = x[k] == top;
-            add_to(mass, count, is ? 0 : SAMPLE_CELLS - 1, is ? 1ull << 50 : 0, on);
+    for (int k = 0; k < SHARE; ++k) {
+        const double v = (double)fmaxf(x[k], lowest), t = fma(v, h.steps, ROUND);
+        const int n = max((int)(uint32_t)(uint64_t)__double_as_longlong(t) - top_n, -2048);
+        const uint64_t w = whole50(power32(n, fma(v, h.steps, ROUND - t)));
+        const int d = (top_n >> 3) - ((top_n + n) >> 3);
+        place[k] = 0xFFFFFFFFu;
+        if (x[k] > -__builtin_inff()) {
+            if (d < SAMPLE_CELLS - 1) {
+                atomicAdd((unsigned long long *)mass + d, (unsigned long long)w);
+                place[k] = (uint32_t)d << 16 | atomicAdd(count + d, 1u);
+            } else {       // the last cell, where masked tokens often are: added once at the end
+                ++last_n;
+                last_w += w;
+            }
+        }
+    }
+    if (last_n) {
+        atomicAdd((unsigned long long *)mass + SAMPLE_CELLS - 1, (unsigned long long)last_w);
+        atomicAdd(count + SAMPLE_CELLS - 1, last_n);
+    }
+    __syncthreads();
+    if (tid < 64) {
+        constexpr int EACH = SAMPLE_CELLS / 64;
+        uint32_t n[EACH], sum = 0;
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) sum += n[e] = count[tid * EACH + e];
+        uint32_t upto = wave_count_scan(sum) - sum;
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            start[tid * EACH + e] = (uint16_t)upto;
+            upto += n[e];
         }
     }
     __syncthreads();
+#pragma unroll
+    for (int k = 0; k < SHARE; ++k)
+        if (place[k] != 0xFFFFFFFFu)
+            list[start[place[k] >> 16] + (place[k] & 0xFFFFu)] = (uint16_t)(wave * VOCAB_CHUNK + share_index(k));
     p.mass[at * SAMPLE_CELLS + tid] = mass[tid];
     p.count[at * SAMPLE_CELLS + tid] = (uint16_t)count[tid];
+    p.start[at * SAMPLE_CELLS + tid] = start[tid];
+    __syncthreads();
+    for (int i = tid * 8; i < start[SAMPLE_CELLS - 1]; i += 256 * 8)
+        *(uint4 *)(p.list + at * SAMPLE_CHUNK + i) = *(const uint4 *)(list + i);
 }
 
 // ------------------------------------------------------------------ the row
 
-// LIST: logits of the cells that matter that are kept in LDS; more are read from the row each time.
-constexpr int ROW_THREADS = 1024, LIST = 8192, STEP_BITS = 10, MOST_CHUNKS = MAX_VOCAB / SAMPLE_CHUNK;
-
-struct RowLds {
-    double upto_mass[SAMPLE_CELLS + 1];                           // of all cells above
-    uint32_t upto_count[SAMPLE_CELLS + 1];
-    uint32_t low[SAMPLE_CELLS], high[SAMPLE_CELLS];               // least and largest key of a cell that is looked at
-    uint8_t want[SAMPLE_CELLS];
-    double factor[MOST_CHUNKS];                                   // of a chunk's weights
-    int below[MOST_CHUNKS];                                       // its first cell
-    uint64_t mass[ROW_THREADS];
-    uint32_t count[ROW_THREADS];
-    uint32_t key[LIST], index[LIST];
-    double wave_mass[16];
-    uint32_t wave_count[16], wave_first[16], wave_last[16];
-    float wave_top[16];
-    double found_mass;
-    uint32_t found_count, found_ties, n, token;
-};
+// LIST: logits of the cells that matter that are kept in LDS; more are read from the row each time. RUNS: of neighbouring cells that
+// matter (those of the three cuts and of the draw). FEW: so many equal or nearly equal logits are compared in a wave's lanes.
+// Sixteen waves, which hide the latency of a list's entries (a cell of some thousand logits takes 40 us with four). What is a chain of
+// a few scalars is left to the first of them. The code runs once through, from memory where other kernels ran in
+// between, so what is not hot is kept short rather than unrolled (53 KB of it took twice the time).
+constexpr int ROW_THREADS = 1024, ROW_WAVES = ROW_THREADS / 64, LIST = 12288, RUNS = 4, FEW = 64;
+constexpr int MOST_CHUNKS = MAX_VOCAB / SAMPLE_CHUNK;
+constexpr int STEP_BITS = 10, STEPS = 1 << STEP_BITS, CELLS_EACH = SAMPLE_CELLS / 64;
+static_assert(STEPS == ROW_THREADS, "a thread has a step, and a pair of chunk and run");
+static_assert(MOST_CHUNKS * RUNS <= ROW_THREADS, "a thread has a step, and a pair of chunk and run");
 
 // A place in the order: a value, how many logits have it, the weight of one, and the weight and number of those above.
 struct Place {
@@ -189,140 +250,225 @@ struct Place {
     double above, weight;
 };
 
+// Cells from .. to, none where to is less.
+struct Span {
+    int from, to;
+    __device__ __forceinline__ bool has(int c) const { return c >= from && c <= to; }
+};
+
+struct RowLds {
+    double upto_mass[SAMPLE_CELLS + 1];                           // of all cells above
+    uint32_t upto_count[SAMPLE_CELLS + 1];
+    uint32_t low[SAMPLE_CELLS], high[SAMPLE_CELLS];               // least and largest key of a cell that is listed
+    double factor[MOST_CHUNKS];                                   // of a chunk's weights
+    int below[MOST_CHUNKS];                                       // its first cell
+    uint64_t mass[STEPS];
+    uint32_t count[STEPS];
+    uint32_t key[LIST], index[LIST];
+    uint32_t run_end[MOST_CHUNKS * RUNS];                         // of a chunk's part of a run in the list
+    uint16_t run_from[MOST_CHUNKS * RUNS];                        // and where the chunk's own list has it
+    uint32_t few_key[FEW];
+    double wave_mass[ROW_WAVES];
+    uint32_t wave_count[ROW_WAVES];
+    int wave_first[ROW_WAVES], wave_last[ROW_WAVES];
+    float wave_top[ROW_WAVES];
+    // what the first wave tells the others
+    Span at[4], runs[RUNS], look;
+    int n_runs, at_once, listed;
+    double goal, found_mass;
+    uint32_t found_count, found_ties, found_key, n, n_few, token;
+};
+
 template <typename L> struct Row {
     const SampleParams &p;
     RowLds &s;
     const typename L::T *logits;
-    RowHeat h;
-    double top_y;
+    double steps, top_g;
     bool in_list;
 
-    __device__ __forceinline__ double y_of(float x) const { return (double)x * h.cells; }
-    __device__ __forceinline__ double weight(uint32_t key) const { return beside(y_of(value_of<L>(key)), top_y); }
-    __device__ __forceinline__ int cell(float x) const { return cells_below(floor(top_y), floor(y_of(x))); }
-
-    // The first cell whose weight with all above it reaches x (or passes it), else the last with logits. In every lane.
-    template <bool PAST> __device__ __forceinline__ int cell_by(double x) const {
-        return first_cell([&](int c) { return PAST ? s.upto_mass[c + 1] > x : s.upto_mass[c + 1] >= x; });
+    __device__ __forceinline__ double weight(uint32_t key) const { return weight_of(value_of<L>(key), steps, top_g); }
+    __device__ __forceinline__ int cell(float x) const { return cells_below(top_g, grid(x, steps)); }
+    // Weights of cell c are below 2^((1 - c) / 4 + 1 / 64), so that whole numbers of 2^-shift add up in 64 bits.
+    __device__ __forceinline__ int shift_of(int c) const {
+        return c / 4 + 29 + __builtin_clz(max(s.upto_count[c + 1] - s.upto_count[c], 1u));
     }
-    template <typename F> __device__ __forceinline__ int first_cell(F yes) const {
+
+    // The first cell up to which the count, or the weight, reaches a goal, else the last with logits. In every lane of a wave.
+    __device__ __forceinline__ int first_cell(bool by_count, double goal) const {
         int first = SAMPLE_CELLS, last = -1;
+        const int c0 = lane_id() * CELLS_EACH;
+        uint32_t n[CELLS_EACH + 1];
+        double m[CELLS_EACH];
 #pragma unroll
-        for (int k = 3; k >= 0; --k) {
-            const int c = lane_id() * 4 + k;
-            const bool some = s.upto_count[c + 1] > s.upto_count[c];
-            if (some && last < 0) last = c;
-            if (some && yes(c)) first = c;
-        }
+        for (int e = 0; e <= CELLS_EACH; ++e) n[e] = s.upto_count[c0 + e];
+#pragma unroll
+        for (int e = 0; e < CELLS_EACH; ++e) m[e] = s.upto_mass[c0 + e + 1];
+#pragma unroll
+        for (int e = CELLS_EACH - 1; e >= 0; --e)
+            if (n[e + 1] > n[e]) {
+                last = max(last, c0 + e);
+                if ((by_count ? (double)n[e + 1] : m[e]) >= goal) first = c0 + e;
+            }
         const uint64_t a = __ballot(first < SAMPLE_CELLS), b = __ballot(last >= 0);
         return a ? __builtin_amdgcn_readlane(first, (int)__builtin_ctzll(a))
                  : __builtin_amdgcn_readlane(last, 63 - (int)__builtin_clzll(b));
     }
 
-    // Lists the logits of the cells from `from` to `to` that s.want names, and finds the bounds of each cell's keys.
-    __device__ void gather(int from, int to) {
-        // no logit of these cells lies outside: y's rounding is below the half cell that is added
-        const double most = (floor(top_y) - from + 1.5) / h.cells, least = (floor(top_y) - to - 0.5) / h.cells;
-        const float hi = top_y == __builtin_inf() || from == 0 ? __builtin_inff() : __double2float_ru(most);
-        // (the lowest number, since -infinity is in no cell)
-        const float lo = top_y == __builtin_inf() ? (to ? -3.4028234e38f : __builtin_inff())
-                         : to == SAMPLE_CELLS - 1 ? -3.4028234e38f : fmaxf(__double2float_rd(least), -3.4028234e38f);
-        const int tid = (int)threadIdx.x;
-        constexpr int DEEP = 8;
-        auto test = [&](typename L::T v, int i, bool on) {
-            const float x = L::value(v);
-            on = on && x >= lo && x <= hi;
-            int c = 0;
-            if (on) {
-                c = cell(x);
-                on = s.want[c];
-            }
-            const uint64_t who = __ballot(on);
-            if (!who) return;
-            uint32_t base = 0;
-            const int leader = (int)__builtin_ctzll(who);
-            if (lane_id() == leader) base = atomicAdd(&s.n, (uint32_t)__popcll(who));
-            base = (uint32_t)__builtin_amdgcn_readlane((int)base, leader);
-            if (on) {
-                const uint32_t key = key_of<L>(v), at = base + (uint32_t)__popcll(who & ((1ull << lane_id()) - 1));
-                if (at < LIST) {
-                    s.key[at] = key;
-                    s.index[at] = (uint32_t)i;
-                }
-                if (key < *(volatile uint32_t *)&s.low[c]) atomicMin(&s.low[c], key);
-                if (key > *(volatile uint32_t *)&s.high[c]) atomicMax(&s.high[c], key);
-            }
-        };
-        const int whole_steps = p.vocab / (ROW_THREADS * 4);
-        int b = 0;
-        for (; b + DEEP <= whole_steps; b += DEEP) {
-            Four<typename L::T> v[DEEP];
-#pragma unroll
-            for (int k = 0; k < DEEP; ++k) v[k] = *(const Four<typename L::T> *)(logits + ((b + k) * ROW_THREADS + tid) * 4);
-#pragma unroll
-            for (int k = 0; k < DEEP; ++k) {
-                float t = L::value(v[k].v[0]);
-                bool near = t >= lo && t <= hi;
-#pragma unroll
-                for (int e = 1; e < 4; ++e) {
-                    t = L::value(v[k].v[e]);
-                    near |= t >= lo && t <= hi;
-                }
-                if (__any(near))
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) test(v[k].v[e], ((b + k) * ROW_THREADS + tid) * 4 + e, true);
+    // The least and largest key of a cell that is listed.
+    __device__ __forceinline__ void bound(int c, uint32_t key) {
+        if (key < *(volatile uint32_t *)&s.low[c]) atomicMin(&s.low[c], key);
+        if (key > *(volatile uint32_t *)&s.high[c]) atomicMax(&s.high[c], key);
+    }
+
+    // Lists the logits of the cells in s.runs (all of them listed by the chunks).
+    __device__ __forceinline__ void collect() {
+        const int tid = (int)threadIdx.x, wave = uniform(tid >> 6), n_runs = uniform(s.n_runs), pairs = p.chunks * n_runs;
+        uint32_t n = 0;
+        if (tid < pairs) {
+            const int c = tid / n_runs, off = s.below[c];
+            const Span run = s.runs[tid - c * n_runs];
+            const int from = max(run.from - off, 0), to = run.to - off;      // of the chunk's cells
+            const int64_t at = (int64_t)blockIdx.x * p.chunks + c;
+            if (off >= 0 && to >= 0) {
+                const uint32_t first = p.start[at * SAMPLE_CELLS + from];
+                n = p.start[at * SAMPLE_CELLS + to] + (uint32_t)p.count[at * SAMPLE_CELLS + to] - first;
+                s.run_from[tid] = (uint16_t)first;
             }
         }
-        for (int i0 = b * ROW_THREADS * 4; i0 < p.vocab; i0 += ROW_THREADS) {
-            const int i = i0 + tid;
-            const bool on = i < p.vocab;
-            test(on ? logits[i] : typename L::T(0), i, on);
+        uint32_t upto = wave_count_scan(n);
+        if (lane_id() == 63) s.wave_count[wave] = upto;
+        __syncthreads();
+        for (int k = 0; k < wave; ++k) upto += s.wave_count[k];
+        if (tid < pairs) s.run_end[tid] = upto;
+        if (tid == pairs - 1) s.n = upto;
+        __syncthreads();
+        const int all = (int)s.n;
+        constexpr int DEEP = 4;                // entries on their way at once
+#pragma unroll 1
+        for (int i0 = tid; i0 < all; i0 += ROW_THREADS * DEEP) {
+            int part[DEEP], at[DEEP];
+            typename L::T v[DEEP];
+#pragma unroll
+            for (int e = 0; e < DEEP; ++e) part[e] = 0;
+#pragma unroll 1
+            for (int step = 512; step; step >>= 1)               // the parts that end at or before the entry
+#pragma unroll
+                for (int e = 0; e < DEEP; ++e)
+                    if (part[e] + step <= pairs - 1 && s.run_end[part[e] + step - 1] <= (uint32_t)(i0 + e * ROW_THREADS))
+                        part[e] += step;
+#pragma unroll
+            for (int e = 0; e < DEEP; ++e) {
+                const int i = min(i0 + e * ROW_THREADS, all - 1), c = part[e] / n_runs;
+                const int from = min(s.run_from[part[e]] + i - (part[e] ? (int)s.run_end[part[e] - 1] : 0), SAMPLE_CHUNK - 1);
+                at[e] = c * SAMPLE_CHUNK + p.list[((int64_t)blockIdx.x * p.chunks + c) * SAMPLE_CHUNK + max(from, 0)];
+            }
+#pragma unroll
+            for (int e = 0; e < DEEP; ++e) v[e] = logits[i0 + e * ROW_THREADS < all ? at[e] : 0];
+#pragma unroll
+            for (int e = 0; e < DEEP; ++e)
+                if (i0 + e * ROW_THREADS < all) {
+                    const uint32_t key = key_of<L>(v[e]);
+                    s.key[i0 + e * ROW_THREADS] = key;
+                    s.index[i0 + e * ROW_THREADS] = (uint32_t)at[e];
+                    bound(cell(L::value(v[e])), key);
+                }
         }
     }
 
-    // f(key, index) of every logit whose key is from lo to hi, in cells that were gathered.
+    // The same for any cells by a pass over the row; where they are more than LIST, the bounds of their keys alone.
+    __device__ __forceinline__ void gather() {
+        const int tid = (int)threadIdx.x;
+        const Span want[RUNS] = {s.runs[0], s.runs[1], s.runs[2], s.runs[3]};
+        float *const stage = (float *)s.mass;
+        constexpr int DEEP = STEPS * 2 / ROW_THREADS;
+#pragma unroll 1
+        for (int i0 = 0; i0 < p.vocab; i0 += ROW_THREADS * DEEP) {
+            typename L::T v[DEEP];
+#pragma unroll
+            for (int e = 0; e < DEEP; ++e) v[e] = logits[min(i0 + e * ROW_THREADS + tid, p.vocab - 1)];
+            // each thread reads back what it wrote
+#pragma unroll
+            for (int e = 0; e < DEEP; ++e) stage[e * ROW_THREADS + tid] = L::value(v[e]);
+#pragma unroll 1
+            for (int e = 0; e < DEEP; ++e) {
+                const int i = i0 + e * ROW_THREADS + tid;
+                const float x = stage[e * ROW_THREADS + tid];
+                int c = 0;
+                bool on = i < p.vocab && x > -__builtin_inff();
+                if (on) {
+                    c = cell(x);
+                    on = want[0].has(c) || want[1].has(c) || want[2].has(c) || want[3].has(c);
+                }
+                const uint64_t who = __ballot(on);
+                if (!who) continue;
+                uint32_t base = 0;
+                const int leader = (int)__builtin_ctzll(who);
+                if (lane_id() == leader) base = atomicAdd(&s.n, (uint32_t)__popcll(who));
+                base = (uint32_t)__builtin_amdgcn_readlane((int)base, leader);
+                if (on) {
+                    const uint32_t key = key_of<L>(logits[i]), at = base + (uint32_t)__popcll(who & ((1ull << lane_id()) - 1));
+                    if (at < LIST) {
+                        s.key[at] = key;
+                        s.index[at] = (uint32_t)i;
+                    }
+                    bound(c, key);
+                }
+            }
+        }
+    }
+
+    // Lists the logits of the cells in s.runs, and finds the bounds of each cell's keys.
+    __device__ __forceinline__ void list() {
+        const int tid = (int)threadIdx.x;
+        if (tid < SAMPLE_CELLS) {
+            s.low[tid] = 0xFFFFFFFFu;
+            s.high[tid] = 0;
+        }
+        if (tid == 0) s.n = 0;
+        __syncthreads();
+        if (s.listed) collect(); else gather();
+        __syncthreads();
+        in_list = s.n <= LIST;
+    }
+
+    // f(key, index) of every logit whose key is from lo to hi, in cells that were listed.
     template <typename F> __device__ __forceinline__ void each(uint32_t lo, uint32_t hi, F f) const {
-        const int tid = (int)threadIdx.x, n = in_list ? (int)s.n : p.vocab;
-        for (int i = tid; i < n; i += ROW_THREADS) {
+        const int n = in_list ? (int)s.n : p.vocab;
+#pragma unroll 1
+        for (int i = (int)threadIdx.x; i < n; i += ROW_THREADS) {
             const uint32_t key = in_list ? s.key[i] : key_of<L>(logits[i]);
             if (key >= lo && key <= hi) f(key, in_list ? s.index[i] : (uint32_t)i);
         }
     }
 
-    // Sums over the threads before each one, the first thread for which `yes` holds of the sums up to it (else the last with a
-    // count), and what lies before that one.
-    template <typename F> __device__ __forceinline__ int first_step(uint32_t n, double m, F yes) {
+    // The first step of s.count and s.mass (in units) for which `yes` holds of the sums up to it, else the last with a count;
+    // in s.found_* what lies before it and its count.
+    template <typename F> __device__ __forceinline__ int first_step(double unit, F yes) {
         const int tid = (int)threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
-        uint32_t upto_n = n;
-        for (int d = 1; d < 64; d <<= 1) {
-            const uint32_t u = (uint32_t)__shfl_up((int)upto_n, d);
-            if (lane >= d) upto_n += u;
-        }
+        const uint32_t n = s.count[tid];
+        const double m = (double)s.mass[tid] * unit;
+        uint32_t upto_n = wave_count_scan(n);
         double upto_m = wave_scan(m);
         if (lane == 63) {
             s.wave_count[wave] = upto_n;
             s.wave_mass[wave] = upto_m;
         }
         __syncthreads();
-        uint32_t before_n = 0;
-        double before_m = 0.0;
+#pragma unroll 1
         for (int k = 0; k < wave; ++k) {
-            before_n += s.wave_count[k];
-            before_m += s.wave_mass[k];
+            upto_n += s.wave_count[k];
+            upto_m += s.wave_mass[k];
         }
-        upto_n += before_n;
-        upto_m += before_m;
         const uint64_t a = __ballot(n && yes(upto_n, upto_m)), b = __ballot(n > 0);
         if (lane == 0) {
-            s.wave_first[wave] = a ? (uint32_t)(wave * 64 + (int)__builtin_ctzll(a)) : ROW_THREADS;
-            s.wave_last[wave] = b ? (uint32_t)(wave * 64 + 64 - (int)__builtin_clzll(b)) : 0;
+            s.wave_first[wave] = a ? tid + (int)__builtin_ctzll(a) : STEPS;
+            s.wave_last[wave] = b ? tid + 63 - (int)__builtin_clzll(b) : -1;
         }
         __syncthreads();
-        const uint32_t f = s.wave_first[lane & 15], l = s.wave_last[lane & 15];
-        const uint64_t c = __ballot(f < ROW_THREADS) & 0xFFFF, d = __ballot(l > 0) & 0xFFFF;
-        int t = 0;
-        if (c) t = __builtin_amdgcn_readlane((int)f, (int)__builtin_ctzll(c));
-        else if (d) t = __builtin_amdgcn_readlane((int)l, 63 - (int)__builtin_clzll(d)) - 1;
+        const int f = s.wave_first[lane & (ROW_WAVES - 1)], l = s.wave_last[lane & (ROW_WAVES - 1)];
+        const uint64_t c = __ballot(f < STEPS) & ((1u << ROW_WAVES) - 1), d = __ballot(l >= 0) & ((1u << ROW_WAVES) - 1);
+        const int t = c ? __builtin_amdgcn_readlane(f, (int)__builtin_ctzll(c))
+                        : d ? __builtin_amdgcn_readlane(l, 63 - (int)__builtin_clzll(d)) : 0;
         if (tid == t) {
             s.found_count = upto_n - n;
             s.found_mass = upto_m - m;
@@ -331,35 +477,84 @@ template <typename L> struct Row {
         __syncthreads();
         return t;
     }
+    __device__ __forceinline__ void clear_steps() {
+        s.mass[threadIdx.x] = 0;
+        s.count[threadIdx.x] = 0;
+        __syncthreads();
+    }
 
-    // The value of cell c at which the running count (BY_COUNT) or weight reaches `goal` (or passes it: PAST).
-    template <bool BY_COUNT, bool PAST> __device__ Place find(int c, double goal) {
-        const int tid = (int)threadIdx.x;
+    // The value of cell c at which the goal is fulfilled.
+    __device__ __forceinline__ Place find(int c, bool by_count, double goal) {
         uint32_t lo = s.low[c], hi = s.high[c];
         Place r;
         r.above = s.upto_mass[c];
         r.above_count = s.upto_count[c];
         r.ties = s.upto_count[c + 1] - r.above_count;
-        // weights of this cell are below 2^(1/8 - c/8) of the largest
-        const int n_bits = 32 - __builtin_clz(max(r.ties, 1u)), shift = c / 8 + 61 - n_bits;
+        const int shift = shift_of(c);
         const double unit = power2(-shift);
-        while (hi > lo) {
+        auto yes = [&](uint32_t n, double m) {
+            return (by_count ? (double)(r.above_count + n) : r.above + m) >= goal;
+        };
+#pragma unroll 1
+        while (hi > lo && r.ties > FEW) {
             const int cut = max(0, 32 - __builtin_clz(hi - lo) - STEP_BITS);
-            s.mass[tid] = 0;
-            s.count[tid] = 0;
-            __syncthreads();
+            clear_steps();
             each(lo, hi, [&](uint32_t key, uint32_t) {
-                add_to(s.mass, s.count, (int)((hi - key) >> cut), whole(weight(key), shift), true);
+                add_to(s.mass, s.count, (int)((hi - key) >> cut), whole(weight(key), shift), value_of<L>(key));
             });
             __syncthreads();
-            const int t = first_step(s.count[tid], (double)s.mass[tid] * unit, [&](uint32_t n, double m) {
-                return BY_COUNT ? (double)(r.above_count + n) >= goal : PAST ? r.above + m > goal : r.above + m >= goal;
-            });
+            const int t = first_step(unit, yes);
             r.above += s.found_mass;
             r.above_count += s.found_count;
             r.ties = s.found_ties;
             hi -= (uint32_t)t << cut;
             lo = max(lo, hi - ((1u << cut) - 1u));
+        }
+        if (hi > lo) {
+            // few are left: a lane each of the first wave, which adds those above it and those of its own value
+            if (threadIdx.x == 0) s.n_few = 0;
+            __syncthreads();
+            each(lo, hi, [&](uint32_t key, uint32_t) {
+                const uint32_t at = atomicAdd(&s.n_few, 1u);
+                if (at < FEW) s.few_key[at] = key;
+            });
+            __syncthreads();
+            if (threadIdx.x < 64) {
+                const int n = min((int)s.n_few, FEW), lane = lane_id();
+                const uint32_t key = lane < n ? s.few_key[lane] : 0;
+                const uint64_t own = lane < n ? whole(weight(key), shift) : 0;
+                const uint32_t own_lo = (uint32_t)own, own_hi = (uint32_t)(own >> 32);
+                uint32_t above = 0, ties = 0;
+                uint64_t above_w = 0, ties_w = 0;
+#pragma unroll 1
+                for (int j = 0; j < n; ++j) {
+                    const uint32_t k = (uint32_t)__builtin_amdgcn_readlane((int)key, j);
+                    const uint64_t w = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)own_hi, j) << 32 |
+                                       (uint32_t)__builtin_amdgcn_readlane((int)own_lo, j);
+                    above += k > key;
+                    above_w += k > key ? w : 0;
+                    ties += k == key;
+                    ties_w += k == key ? w : 0;
+                }
+                // the largest that fulfils the goal with all of its value, else the least
+                const bool on = lane < n, enough = on && yes(above + ties, (double)(above_w + ties_w) * unit);
+                const uint64_t any = __ballot(enough);
+                uint32_t best = any ? (enough ? key : 0) : (on ? ~key : 0);
+                for (int d = 32; d; d >>= 1) best = max(best, (uint32_t)__shfl_xor((int)best, d));
+                if (!any) best = ~best;
+                if (lane == (int)__builtin_ctzll(__ballot(on && key == best))) {
+                    s.found_key = best;
+                    s.found_mass = (double)above_w * unit;
+                    s.found_count = above;
+                    s.found_ties = ties;
+                }
+            }
+            __syncthreads();
+            hi = s.found_key;
+            r.above += s.found_mass;
+            r.above_count += s.found_count;
+            r.ties = s.found_ties;
+            __syncthreads();
         }
         r.key = hi;
         r.weight = weight(hi);
@@ -367,23 +562,22 @@ template <typename L> struct Row {
     }
 
     // The index of the t-th (from 0) of the logits whose key is `key`, of which there are `ties`.
-    __device__ uint32_t nth_index(uint32_t key, uint32_t t, uint32_t ties) {
-        const int tid = (int)threadIdx.x;
+    __device__ __forceinline__ uint32_t nth_index(uint32_t key, uint32_t t, uint32_t ties) {
         if (ties == 1) {
             each(key, key, [&](uint32_t, uint32_t at) { s.token = at; });
             __syncthreads();
             return s.token;
         }
         uint32_t lo = 0, hi = (uint32_t)p.vocab - 1;
+#pragma unroll 1
         while (hi > lo) {
             const int cut = max(0, 32 - __builtin_clz(hi - lo) - STEP_BITS);
-            s.count[tid] = 0;
-            __syncthreads();
+            clear_steps();
             each(key, key, [&](uint32_t, uint32_t at) {
                 if (at >= lo && at <= hi) atomicAdd(&s.count[(at - lo) >> cut], 1u);
             });
             __syncthreads();
-            const int f = first_step(s.count[tid], 0.0, [&](uint32_t n, double) { return n > t; });
+            const int f = first_step(0.0, [&](uint32_t n, double) { return n > t; });
             t -= min(t, s.found_count);
             lo += (uint32_t)f << cut;
             hi = min(hi, lo + ((1u << cut) - 1u));
@@ -394,20 +588,20 @@ template <typename L> struct Row {
 
 template <typename L> __global__ void __launch_bounds__(ROW_THREADS) moe_sample_row_kernel(SampleParams p) {
     __shared__ RowLds s;
-    const int row = (int)blockIdx.x, tid = (int)threadIdx.x, lane = lane_id(), group = tid >> 8, cell = tid & 255;
-    const RowHeat h = row_heat(p, row);
-    SampleHead head = {0.0, -__builtin_inff(), 0};
+    const int row = (int)blockIdx.x, tid = (int)threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);
+    SampleHead head = {0.0, -__builtin_inff(), 1};
     if (tid < p.chunks) head = p.head[(int64_t)row * p.chunks + tid];
-    if (tid < SAMPLE_CELLS) {
-        s.want[tid] = 0;
-        s.low[tid] = 0xFFFFFFFFu;
-        s.high[tid] = 0;
-    }
-    if (tid == 0) s.n = 0;
-    float top = wave_max(head.top);
-    if (lane == 0) s.wave_top[tid >> 6] = top;
+    const RowHeat h = row_heat(p, row);
+    // what is asked for, in scalar registers
+    const int asked_k = p.top_k ? uniform(p.top_k[row]) : 0;
+    auto scalar = [](float v) { return __int_as_float(uniform(__float_as_int(v))); };
+    const float top_p = p.top_p ? scalar(p.top_p[row]) : 1.0f, asked_m = p.min_p ? scalar(p.min_p[row]) : 0.0f;
+    const float min_p = asked_m > 1.0f ? 1.0f : asked_m, given = scalar(p.u[row]);
+    const double u = (double)(given > 0.0f ? fminf(given, 0.99999994f) : 0.0f);
+    float top = wave_max(head.top);      // (only the first waves have chunks)
+    if (lane == 0) s.wave_top[wave] = top;
     fill_exp_table();
-    top = wave_max(s.wave_top[lane & 15]);
+    top = wave_max(s.wave_top[lane & (ROW_WAVES - 1)]);
     if (!(top > -__builtin_inff())) {
         if (tid == 0) {
             raise_flag(p.flags, MOE_FLAG_LOGITS);
@@ -416,161 +610,241 @@ template <typename L> __global__ void __launch_bounds__(ROW_THREADS) moe_sample_
         }
         return;
     }
-    const double top_y = (double)top * h.cells;
+    const double top_g = grid(top, h.steps);
     if (tid < p.chunks) {
         const bool some = head.top > -__builtin_inff();
-        s.below[tid] = some ? cells_below(floor(top_y), floor(head.top_y)) : -1;
-        s.factor[tid] = some ? beside(head.top_y, top_y) * power2(-50) : 0.0;
+        s.below[tid] = some ? cells_below(top_g, head.top_g) : -1;
+        s.factor[tid] = !some ? 0.0 : head.top_g == top_g ? power2(-50) : power32_of(head.top_g - top_g) * power2(-50);
     }
-    __syncthreads();
-    // the chunks' cells on the row's: thread (group, cell) takes every fourth chunk; what goes into the last cell from
-    // elsewhere is added by all threads
+    // whether the chunks of the row listed their logits
+    const bool listed = !__syncthreads_or(!head.listed && head.top > -__builtin_inff());
+    // The chunks' cells on the row's, a thread each for every fourth chunk. A chunk whose largest logit is `off` cells down has
+    // its cells that much later; the threads before that take those that would lie past the last cell, which are added to it.
     double m = 0.0, tail = 0.0;
     uint32_t n = 0, tail_n = 0;
     const int64_t base = (int64_t)row * p.chunks * SAMPLE_CELLS;
-#pragma unroll 8
-    for (int c = group; c < p.chunks; c += 4) {
-        const int off = s.below[c], from = cell - off;
-        const bool here = off >= 0 && from >= 0;
-        const int64_t at = base + (int64_t)c * SAMPLE_CELLS + (here ? from : 0);
-        const uint64_t w = p.mass[at];
-        const uint32_t k = p.count[at];
-        if (here && cell < SAMPLE_CELLS - 1) {
-            m += (double)w * s.factor[c];
-            n += k;
-        }
-        if (off >= 0 && cell + off >= SAMPLE_CELLS - 1) {
-            tail += (double)p.mass[base + (int64_t)c * SAMPLE_CELLS + cell] * s.factor[c];
-            tail_n += p.count[base + (int64_t)c * SAMPLE_CELLS + cell];
-        }
-    }
-    s.count[tid] = n;
-    ((double *)s.mass)[tid] = m;
-    tail = wave_sum(tail);
-    for (int d = 32; d; d >>= 1) tail_n += (uint32_t)__shfl_xor((int)tail_n, d);
-    if (lane == 0) {
-        s.wave_mass[tid >> 6] = tail;
-        s.wave_count[tid >> 6] = tail_n;
-    }
-    __syncthreads();
-    if (tid < 64) {
-        double w[4], sum = 0.0;
-        uint32_t k[4], sum_n = 0;
+    constexpr int DEEP = 8, GROUPS = ROW_THREADS / SAMPLE_CELLS;
+    const int group = tid / SAMPLE_CELLS, cell = tid & (SAMPLE_CELLS - 1);
+#pragma unroll 1
+    for (int c0 = group; c0 < p.chunks; c0 += DEEP * GROUPS) {
+        uint64_t w[DEEP];
+        uint32_t q[DEEP];
+        int off[DEEP];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int c = tid * 4 + e;
+        for (int e = 0; e < DEEP; ++e) off[e] = c0 + e * GROUPS < p.chunks ? s.below[c0 + e * GROUPS] : -1;
+#pragma unroll
+        for (int e = 0; e < DEEP; ++e) {      // all on their way before the first is used
+            const int at = min(c0 + e * GROUPS, p.chunks - 1) * SAMPLE_CELLS + ((cell - off[e]) & (SAMPLE_CELLS - 1));
+            w[e] = p.mass[base + at];
+            q[e] = p.count[base + at];
+        }
+#pragma unroll
+        for (int e = 0; e < DEEP; ++e) {
+            if (off[e] < 0) continue;         // a chunk without logits: its cells were not written
+            const double v = (double)w[e] * s.factor[c0 + e * GROUPS];
+            const bool own = cell >= off[e];
+            m += own ? v : 0.0;
+            n += own ? q[e] : 0;
+            tail += own ? 0.0 : v;
+            tail_n += own ? 0 : q[e];
+        }
+    }
+    tail = wave_sum(tail);
+    tail_n = (uint32_t)__builtin_amdgcn_readlane((int)wave_count_scan(tail_n), 63);
+    if (lane == 0) {
+        s.wave_mass[wave] = tail;
+        s.wave_count[wave] = tail_n;
+    }
+    ((double *)s.mass)[tid] = m;
+    s.count[tid] = n;
+    __syncthreads();
+    enum { K, P, M, D };
+    const uint32_t k = h.greedy ? 1u : asked_k > 0 ? (uint32_t)asked_k : 0xFFFFFFFFu;
+    const double least_weight = (double)min_p * weight_of(top, h.steps, top_g);
+    Row<L> r = {p, s, row_of<L>(p, row), h.steps, top_g, true};
+    // what has to be reached, where `left` is left by the cuts before: the draw passes its part of that, and so reaches the next number
+    auto goal_of = [&](int i, double left) {
+        return i == K ? (double)k : i == P ? (double)top_p * left
+                                           : __longlong_as_double(__double_as_longlong(u * left) + 1);
+    };
+    // which of them there are, a bit each
+    int by = (!h.greedy && top_p < 1.0f) << P | (!h.greedy && min_p > 0.0f) << M | 1 << D;
+    if (wave == 0) {
+        double w[CELLS_EACH], sum = 0.0;
+        uint32_t q[CELLS_EACH], sum_n = 0;
+#pragma unroll
+        for (int e = 0; e < CELLS_EACH; ++e) {
+            const int c = lane * CELLS_EACH + e;
             w[e] = 0.0;
-            k[e] = 0;
-            for (int g = 0; g < 4; ++g) {
-                w[e] += ((double *)s.mass)[g * 256 + c];
-                k[e] += s.count[g * 256 + c];
+            q[e] = 0;
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) {
+                w[e] += ((double *)s.mass)[g * SAMPLE_CELLS + c];
+                q[e] += s.count[g * SAMPLE_CELLS + c];
             }
-            if (c == SAMPLE_CELLS - 1)
-                for (int g = 0; g < 16; ++g) {
-                    w[e] += s.wave_mass[g];
-                    k[e] += s.wave_count[g];
-                }
+        }
+        const double tails = wave_sum(lane < ROW_WAVES ? s.wave_mass[lane & (ROW_WAVES - 1)] : 0.0);
+        const uint32_t tails_n = (uint32_t)__builtin_amdgcn_readlane(
+            (int)wave_count_scan(lane < ROW_WAVES ? s.wave_count[lane & (ROW_WAVES - 1)] : 0), 63);
+        if (lane == 63) {
+            w[CELLS_EACH - 1] += tails;
+            q[CELLS_EACH - 1] += tails_n;
+        }
+#pragma unroll
+        for (int e = 0; e < CELLS_EACH; ++e) {
             sum += w[e];
-            sum_n += k[e];
+            sum_n += q[e];
         }
         double before = wave_scan(sum) - sum;
-        uint32_t upto = sum_n;
-        for (int d = 1; d < 64; d <<= 1) {
-            const uint32_t u = (uint32_t)__shfl_up((int)upto, d);
-            if (tid >= d) upto += u;
-        }
-        uint32_t before_n = upto - sum_n;
+        uint32_t before_n = wave_count_scan(sum_n) - sum_n;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            s.upto_mass[tid * 4 + e] = before;
-            s.upto_count[tid * 4 + e] = before_n;
+        for (int e = 0; e < CELLS_EACH; ++e) {
+            s.upto_mass[lane * CELLS_EACH + e] = before;
+            s.upto_count[lane * CELLS_EACH + e] = before_n;
             before += w[e];
-            before_n += k[e];
+            before_n += q[e];
         }
-        if (tid == 63) {
+        if (lane == 63) {
             s.upto_mass[SAMPLE_CELLS] = before;
             s.upto_count[SAMPLE_CELLS] = before_n;
         }
-    }
-    __syncthreads();
-    const double all = s.upto_mass[SAMPLE_CELLS];
-    Row<L> r = {p, s, row_of<L>(p, row), h, top_y, true};
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 
-    // the cells that the cuts and the draw fall into: of top-p and the draw a first and a last one, since what the cuts before
-    // them leave is known to a cell only
-    const uint32_t k = h.greedy ? 1u : p.top_k && p.top_k[row] > 0 ? (uint32_t)p.top_k[row] : 0xFFFFFFFFu;
-    const float top_p = p.top_p ? p.top_p[row] : 1.0f, asked = p.min_p ? p.min_p[row] : 0.0f;
-    const float min_p = asked > 1.0f ? 1.0f : asked, given = p.u[row];
-    const double u = (double)(given > 0.0f ? fminf(given, 0.99999994f) : 0.0f);
-    const bool by_k = k < s.upto_count[SAMPLE_CELLS], by_p = !h.greedy && top_p < 1.0f, by_m = !h.greedy && min_p > 0.0f;
-    const int k_cell = by_k ? r.first_cell([&](int c) { return s.upto_count[c + 1] >= k; }) : 0;
-    double least = all, most = all;
-    if (by_k) least = s.upto_mass[k_cell], most = s.upto_mass[k_cell + 1];
-    int p_from = 0, p_to = -1, m_cell = 0;
-    if (by_p) {
-        p_from = r.template cell_by<false>((double)top_p * least);
-        p_to = r.template cell_by<false>((double)top_p * most);
-        least = fmin(least, s.upto_mass[p_from]);
-        most = fmin(most, s.upto_mass[p_to + 1]);
+        // The cells that the cuts and the draw fall into: but for top-k a first and a last one, since what the cuts before them
+        // leave (and for min-p its place) is not known to more than a cell yet.
+        by |= k < s.upto_count[SAMPLE_CELLS] ? 1 << K : 0;
+        if (lane < 4) s.at[lane] = {1, 0};
+        double least = s.upto_mass[SAMPLE_CELLS], most = least;
+#pragma unroll 1
+        for (int i = K; i <= D; ++i) {
+            if (!(by >> i & 1)) continue;
+            Span c;
+            if (i == M) {
+                // the logarithm in 32 bits is within 1/100 of a step
+                const double g = top_g + (double)(32.0f * __log2f((float)least_weight));
+                c = {cells_below(top_g, g + 0.75), cells_below(top_g, g - 0.75)};
+                if (top_g == __builtin_inf()) c = {0, 0};
+            } else {
+#pragma unroll 1
+                for (int end = 0; end < 2; ++end) {
+                    const int f = r.first_cell(i == K, goal_of(i, end ? most : least));
+                    if (!end) c.from = f;
+                    c.to = f;
+                }
+            }
+            s.at[i] = c;
+            least = fmin(least, s.upto_mass[c.from]);
+            most = fmin(most, s.upto_mass[c.to + 1]);
+        }
+        // as runs of neighbouring cells, in their order: the next one begins at the least cell that is left
+        int n_runs = 0, last = 0;
+        uint32_t in_runs = 0;
+        const Span at[4] = {s.at[K], s.at[P], s.at[M], s.at[D]};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            last = max(last, at[i].to);
+            s.runs[i] = {1, 0};
+        }
+#pragma unroll 1
+        for (int c = 0; n_runs < RUNS;) {
+            int from = SAMPLE_CELLS;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (at[i].to >= c && at[i].from <= at[i].to) from = min(from, max(at[i].from, c));
+            if (from == SAMPLE_CELLS) break;
+            int to = from;
+#pragma unroll 1
+            for (int again = 0; again < RUNS; ++again)         // as often as there are parts that may go on where another ends
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (at[i].from <= to + 1 && at[i].to > to) to = at[i].to;
+            s.runs[n_runs++] = {from, to};
+            in_runs += s.upto_count[to + 1] - s.upto_count[from];
+            c = to + 1;
+        }
+        // all of them listed at once where they fit, else those of one cut after the other
+        s.n_runs = n_runs;
+        s.at_once = in_runs <= LIST;
+        s.listed = listed && last < SAMPLE_CELLS - 1;
     }
-    double floor_y = 0.0;
-    if (by_m) {
-        // the cell that the least weight lies in
-        floor_y = top_y == __builtin_inf() ? top_y : top_y + 8.0 * log2((double)min_p);
-        m_cell = cells_below(floor(top_y), floor(floor_y));
-        least = fmin(least, s.upto_mass[m_cell]);
-        most = fmin(most, s.upto_mass[m_cell + 1]);
-    }
-    const int d_from = r.template cell_by<true>(u * least), d_to = r.template cell_by<true>(u * most);
-    int from = d_from, to = d_to;
-    if (by_k) from = min(from, k_cell), to = max(to, k_cell);
-    if (by_p) from = min(from, p_from), to = max(to, p_to);
-    if (by_m) from = min(from, m_cell), to = max(to, m_cell);
-    if (tid < SAMPLE_CELLS)
-        s.want[tid] = (tid >= d_from && tid <= d_to) || (by_k && tid == k_cell) || (by_p && tid >= p_from && tid <= p_to) ||
-                      (by_m && tid == m_cell);
     __syncthreads();
-    r.gather(from, to);
-    __syncthreads();
-    r.in_list = s.n <= LIST;
+    by |= k < s.upto_count[SAMPLE_CELLS] ? 1 << K : 0;
+    const double all = s.upto_mass[SAMPLE_CELLS];
+    const bool at_once = s.at_once;
+    bool have = false;
 
     double kept = all;
-    if (by_k) {
-        const Place at = r.template find<true, false>(k_cell, (double)k);
-        kept = at.above + (double)(k - at.above_count) * at.weight;
-    }
-    if (by_p) {
-        const double goal = (double)top_p * kept;
-        const Place at = r.template find<false, false>(min(max(r.template cell_by<false>(goal), p_from), p_to), goal);
-        const double ties = at.weight > 0.0 ? ceil((goal - at.above) / at.weight) : 1.0;
-        kept = fmin(kept, at.above + fmin(fmax(ties, 1.0), (double)at.ties) * at.weight);
-    }
-    if (by_m) {
-        // the part of its cell that is not below the least weight
-        const uint32_t count = s.upto_count[m_cell + 1] - s.upto_count[m_cell];
-        const int n_bits = 32 - __builtin_clz(max(count, 1u)), shift = m_cell / 8 + 61 - n_bits;
-        if (tid == 0) s.mass[0] = 0;
+    Place found = {};
+    double goal = 0.0;
+#pragma unroll 1
+    for (int i = K; i <= D; ++i) {
+        if (!(by >> i & 1)) continue;
+        if (wave == 0) {
+            s.goal = goal_of(i, kept);
+            Span c = s.at[i];
+            if (i != M) c.from = c.to = min(max(r.first_cell(i == K, goal_of(i, kept)), c.from), c.to);
+            s.look = c;
+            if (!at_once) {
+                s.runs[0] = c;
+                s.runs[1] = s.runs[2] = s.runs[3] = {1, 0};
+                s.n_runs = 1;
+                s.listed = listed && c.to < SAMPLE_CELLS - 1 && s.upto_count[c.to + 1] - s.upto_count[c.from] <= LIST;
+            }
+        }
         __syncthreads();
-        uint64_t sum = 0;
-        if (count)
-            r.each(s.low[m_cell], s.high[m_cell], [&](uint32_t key, uint32_t) {
-                const double w = r.weight(key);
-                if (w >= (double)min_p) sum += whole(w, shift);
-            });
-        for (int d = 32; d; d >>= 1) sum += (uint64_t)__shfl_xor((long long)sum, d);
-        if (lane == 0 && sum) atomicAdd((unsigned long long *)s.mass, (unsigned long long)sum);
-        __syncthreads();
-        kept = fmin(kept, s.upto_mass[m_cell] + (double)s.mass[0] * power2(-shift));
+        const Span c = s.look;
+        goal = s.goal;
+        if (i == K && s.upto_mass[c.to + 1] == s.upto_mass[c.from]) {      // a cut among weights of nothing
+            kept = s.upto_mass[c.from];
+            __syncthreads();
+            continue;
+        }
+        if (!have) {
+            r.list();
+            have = at_once;
+        }
+        if (i == M) {
+            // the part of its cells that is not below the least weight
+            double sum = 0.0;
+#pragma unroll 1
+            for (int b = c.from; b <= c.to; ++b) {
+                if (s.upto_count[b + 1] == s.upto_count[b]) continue;
+                const int shift = r.shift_of(b);
+                if (tid == 0) s.mass[0] = 0;
+                __syncthreads();
+                uint64_t w = 0;
+                r.each(s.low[b], s.high[b], [&](uint32_t key, uint32_t) {
+                    const double v = r.weight(key);
+                    w += v >= least_weight ? whole(v, shift) : 0;
+                });
+                if (w) atomicAdd((unsigned long long *)s.mass, (unsigned long long)w);
+                __syncthreads();
+                sum += (double)s.mass[0] * power2(-shift);
+                __syncthreads();
+            }
+            kept = fmin(kept, s.upto_mass[c.from] + sum);
+            __syncthreads();
+            continue;
+        }
+        found = r.find(c.from, i == K, goal);
+        // how many of that value are left
+        const double need = i == K ? (double)(k - found.above_count) : ((i == D ? u * kept : goal) - found.above) / found.weight;
+        if (i == D) {
+            goal = need;
+            break;
+        }
+        kept = fmin(kept, found.above + fmin(fmax(ceil(need), 1.0), (double)found.ties) * found.weight);
         __syncthreads();
     }
-    const double goal = u * kept;
-    const Place at = r.template find<false, true>(min(max(r.template cell_by<true>(goal), d_from), d_to), goal);
-    const double t = at.weight > 0.0 ? floor((goal - at.above) / at.weight) : 0.0;
-    const uint32_t token = r.nth_index(at.key, (uint32_t)fmin(fmax(t, 0.0), (double)(at.ties - 1)), at.ties);
+    const uint32_t token = r.nth_index(found.key, (uint32_t)fmin(fmax(floor(goal), 0.0), (double)(found.ties - 1)), found.ties);
     if (tid == 0) {
-        const double y = r.y_of(value_of<L>(at.key));
         p.tokens[row] = (int32_t)token;
-        p.logprobs[row] = h.greedy ? 0.0f : (float)((y == top_y ? 0.0 : (y - top_y) * 0.08664339756999316) - log(all));
+        // the logarithm of the rounded share, and of what the rounding left
+        const double share = found.weight / all;
+        const float near = (float)share;
+        p.logprobs[row] = h.greedy ? 0.0f : logf(near) + (float)(share - (double)near) / near;
     }
 }
 
