@@ -75,17 +75,22 @@ __device__ __forceinline__ int cells_below(double top, double g) {
 // 2^((k + r) / 32) for a whole k <= 0 and |r| <= 1/2, to about 2^-48: 2^(k / 32) from a table (its entries lie on different
 // banks of LDS) and the exponent, times the Taylor polynomial of degree 5 of e^(r log(2) / 32), whose remainder is below
 // 3e-15 of the value where r is largest.
-__device__ __forceinline__ double power32(int k, double r) {
-    constexpr double C = 0.02166084939249829;     // log(2) / 32
-    const double m = exp_table()[k & 31];
-    double e = fma(r, C * C * C * C * C / 120.0, C * C * C * C / 24.0);
-    e = fma(e, r, C * C * C / 6.0);
-    e = fma(e, r, C * C / 2.0);
-    e = fma(e, r, C);
-    e = fma(m, e * r, m);
-    const uint64_t bits = (uint64_t)__double_as_longlong(e) + ((uint64_t)(uint32_t)((k >> 5) * (1 << 20)) << 32);
-    return __longlong_as_double((long long)bits);
-}
+struct Power32 {
+    // the coefficients, kept in scalar registers
+    double c1 = 0.02166084939249829, c2 = c1 * c1 / 2.0, c3 = c1 * c1 * c1 / 6.0, c4 = c1 * c1 * c1 * c1 / 24.0,
+           c5 = c1 * c1 * c1 * c1 * c1 / 120.0;     // c1: log(2) / 32
+    __device__ __forceinline__ Power32() { asm("" : "+s"(c1), "+s"(c2), "+s"(c3), "+s"(c4), "+s"(c5)); }
+    __device__ __forceinline__ double operator()(int k, double r) const {
+        const double m = exp_table()[k & 31];
+        double e = fma(r, c5, c4);
+        e = fma(e, r, c3);
+        e = fma(e, r, c2);
+        e = fma(e, r, c1);
+        e = fma(m, e * r, m);
+        return __hiloint2double(__double2hiint(e) + ((k >> 5) * (1 << 20)), __double2loint(e));
+    }
+};
+__device__ __forceinline__ double power32(int k, double r) { return Power32()(k, r); }
 // Weights are in 2^(top / 32), top being the largest logit's place on the grid. Where that is infinite, all weight is
 // on it. What lies 64 octaves below weighs nothing.
 __device__ __forceinline__ double weight_of(float x, double steps, double top) {
@@ -162,7 +167,7 @@ template <typename L> __global__ void __launch_bounds__(256) moe_sample_cells_ke
     const double top_g = grid(top, h.steps);
     // Two kinds of chunks are taken slowly, and not listed: with an infinite logit, or a temperature next to 0 (places that 32 bits
     // do not hold); with many equal logits (a wave's first ones), whose additions at one place would take one after another
-    const float lowest = (float)((top_g - 2048.0) / h.steps);      // what lies below weighs nothing
+    const float lowest = (float)((top_g - 2304.0) / h.steps);      // what lies below weighs nothing
     const bool equal = x[0] > lowest && __ballot(x[0] == __int_as_float(uniform(__float_as_int(x[0])))) == ~0ull;
     const bool slow = __syncthreads_or(equal || !(fabs(top_g) < 0x1p29)) != 0;
     if (tid == 0) p.head[at] = {top_g, top, !slow};
@@ -179,32 +184,26 @@ template <typename L> __global__ void __launch_bounds__(256) moe_sample_cells_ke
         p.count[at * SAMPLE_CELLS + tid] = (uint16_t)count[tid];
         return;
     }
-    // Cell and number within it; a logit in the last cell has none. Places on the grid are 32-bit whole numbers.
-    // What lies far below, or is a NaN, is taken to 2048 steps below the top, where it weighs nothing.
+    // Cell and number within it; a logit in the last cell has none. Places on the grid are 32-bit whole numbers. What lies far
+    // below, or is a NaN, is taken to the last cell, where a weight is nothing in 2^-50.
     uint32_t place[SHARE], last_n = 0;
-    uint64_t last_w = 0;
-    const int top_n = (int)top_g;
+    const int top_n = (int)top_g, top_d = top_n >> 3;
+    const Power32 power;
 #pragma unroll
     for (int k = 0; k < SHARE; ++k) {
         const double v = (double)fmaxf(x[k], lowest), t = fma(v, h.steps, ROUND);
-        const int n = max((int)(uint32_t)(uint64_t)__double_as_longlong(t) - top_n, -2048);
-        const uint64_t w = whole50(power32(n, fma(v, h.steps, ROUND - t)));
-        const int d = (top_n >> 3) - ((top_n + n) >> 3);
-        place[k] = 0xFFFFFFFFu;
-        if (x[k] > -__builtin_inff()) {
-            if (d < SAMPLE_CELLS - 1) {
-                atomicAdd((unsigned long long *)mass + d, (unsigned long long)w);
-                place[k] = (uint32_t)d << 16 | atomicAdd(count + d, 1u);
-            } else {       // the last cell, where masked tokens often are: added once at the end
-                ++last_n;
-                last_w += w;
-            }
+        const int n = max((int)(uint32_t)(uint64_t)__double_as_longlong(t), top_n - 2048);
+        const uint64_t w = whole50(power(n - top_n, fma(v, h.steps, ROUND - t)));
+        place[k] = (uint32_t)(top_d - (n >> 3));
+        if (place[k] < SAMPLE_CELLS - 1) {
+            atomicAdd((unsigned long long *)mass + place[k], (unsigned long long)w);
+            place[k] = place[k] << 16 | atomicAdd(count + place[k], 1u);
+        } else {       // the last cell, where masked tokens often are: added once at the end
+            place[k] = 0xFFFFFFFFu;
+            last_n += x[k] > -__builtin_inff();
         }
     }
-    if (last_n) {
-        atomicAdd((unsigned long long *)mass + SAMPLE_CELLS - 1, (unsigned long long)last_w);
-        atomicAdd(count + SAMPLE_CELLS - 1, last_n);
-    }
+    if (last_n) atomicAdd(count + SAMPLE_CELLS - 1, last_n);
     __syncthreads();
     if (tid < 64) {
         constexpr int EACH = SAMPLE_CELLS / 64;
