@@ -307,6 +307,15 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
             t_last = min(t_last, (int)(((int64_t)len + i_last + 64) >> 6));
         }
 
+        const int32_t *table = p.c.table + (SHARED ? uniform(sq.seq) : b) * p.c.table_stride;
+        // The pages of this wave's group of 64 tiles, a lane each, looked up 64 tiles before they are needed: loads come back in
+        // their order, and a look-up for each tile would have to wait for the tile before it.
+        auto pages_of = [&](int tile) {
+            const int64_t t = ((int64_t)tile + lane) * 64 + wave * 16;      // a tile past the last may lie past 2^31
+            return t < end ? table[(int)t / p.c.page] : -1;
+        };
+        int pages_from = first_tile, pages = pages_of(first_tile), pages_next = pages_of(first_tile + 64);
+
         s16x8 qf[NQ][KS];
         uint64_t mask[NQ];
         int late[NQ];                     // the last row past the 64th that is seen
@@ -344,13 +353,15 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
             return (int)(j < 0) | ((int)(j < 64) & (int)(mask[u] >> (j & 63)) & 1) | ((int)(j >= 64) & (int)(j <= late[u]));
         };
 
-        const int32_t *table = p.c.table + (SHARED ? uniform(sq.seq) : b) * p.c.table_stride;
         u32x4 kr[LOADS], vr[LOADS];
         uint32_t ksr[LOADS], vsr[LOADS];
-        // the page of this wave's group of a tile; looked up a tile before it is needed
-        auto page_of = [&](int tile) {
-            const int64_t t = (int64_t)tile * 64 + wave * 16;      // a tile past the last may lie past 2^31
-            return t < end ? table[(int)t / p.c.page] : -1;
+        auto page_of = [&](int tile) {       // tiles in their order
+            if (tile - pages_from == 64) {
+                pages = pages_next;
+                pages_from = tile;
+                pages_next = pages_of(tile + 64);
+            }
+            return __builtin_amdgcn_readlane(pages, tile - pages_from);
         };
         // A group without a page reads the first one's slots instead: its scores are masked and its values zeroed.
         auto load = [&](int tile, int page) {
@@ -378,23 +389,26 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
             return ok || t >= end;
         };
 
-        int page = first_tile < t_last ? uniform(page_of(first_tile)) : 0;
         bool good = true;
-        if (first_tile < t_last) {
-            good = load(first_tile, page);
-            page = page_of(first_tile + 1);
-        }
+        if (first_tile < t_last) good = load(first_tile, page_of(first_tile));
         for (int tile = first_tile; tile < t_last; ++tile) {
             const int buf = tile & 1, t0 = tile * 64;
             uint16_t *const kl = lds[buf][0], *const vl = lds[buf][1];
             int told = good ? 0 : 1;
             // what a loaded piece stands for, in 16 bits
-            u32x4 kx[LOADS][SPREAD], vx[LOADS][SPREAD];
+            u32x4 vx[LOADS][SPREAD];
 #pragma unroll
             for (int k = 0; k < LOADS; ++k) {
-                mx_expand<F16, FMT>(kr[k], ksr[k], kx[k]);
-                mx_expand<F16, FMT>(vr[k], vsr[k], vx[k]);
+                u32x4 kx[SPREAD];
+                mx_expand<F16, FMT>(kr[k], ksr[k], kx);
+                if (!RAGGED || k * 64 + lane < PIECES) {
+#pragma unroll
+                    for (int s = 0; s < SPREAD; ++s)
+                        *(u32x4 *)(kl + wave * GE + k_place<D>(pt[k], pc[k] + s)) = kx[s];
+                }
             }
+#pragma unroll
+            for (int k = 0; k < LOADS; ++k) mx_expand<F16, FMT>(vr[k], vsr[k], vx[k]);
             if (t0 + wave * 16 + 16 > len || !good) {
                 // the step's own tokens: slots behind the last hold anything, and are zeroed; a value that is not finite
                 // must not reach the rows that do not see it
@@ -416,15 +430,11 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
 #pragma unroll
                     for (int s = 0; s < SPREAD; ++s) {
                         const int c = pc[k] + s;
-                        *(u32x4 *)(kl + wave * GE + k_place<D>(pt[k], c)) = kx[k][s];
                         *(u32x4 *)(vl + wave * GE + v_unit<D>(pt[k], c >> 1) + (c & 1) * 8) = vx[k][s];
                     }
                 }
             if (lane == 0) note[buf][wave] = told;
-            if (tile + 1 < t_last) {
-                good = load(tile + 1, uniform(page));
-                page = page_of(tile + 2);
-            }
+            if (tile + 1 < t_last) good = load(tile + 1, page_of(tile + 1));
             __syncthreads();
             const int4 notes = *(const int4 *)note[buf];
             const int all = uniform(notes.x | notes.y << 4 | notes.z << 8 | notes.w << 12);   // four bits a group

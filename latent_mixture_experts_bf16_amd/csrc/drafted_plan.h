@@ -59,8 +59,8 @@ struct AppendParams {
     const void *q_weight, *k_weight;
     int64_t qw_stride, kw_stride;
     int32_t norm;               // moe_dtype of the weights, 0: no norm
-    float eps, offset;
-    int32_t half, wide;         // layout; every row 16-byte aligned
+    float eps, offset, inv_dim;
+    int32_t half, wide, wide_weights;   // layout; every row, and every head's weights, 16-byte aligned
     int32_t lanes;              // that hold a head, eight dims each: a power of two
 };
 

@@ -48,13 +48,17 @@ class HeadNorm:
         qs, ks = (w.stride(0) if w.dim() == 2 and w.shape[0] > 1 else 0 for w in (q_weight, k_weight))
         self._c = B.moe_head_norm(q_weight.data_ptr(), k_weight.data_ptr(), qs, ks, _DT[q_weight.dtype], eps, offset)
         self._ref = ctypes.addressof(self._c)
+        self._fits = None
 
     def _check(self, device: torch.device, index: int, heads: int, kv_heads: int, dim: int) -> None:
+        if self._fits == (index, heads, kv_heads, dim):      # the weights do not change
+            return
         for name, w, n in (("q_weight", self.q_weight, heads), ("k_weight", self.k_weight, kv_heads)):
             if w.shape[-1] != dim or (w.dim() == 2 and w.shape[0] != n):
                 _refuse(_SHAPE, f"norm {name}: shape {tuple(w.shape)}, expected ({dim},) or ({n}, {dim})")
             if w.get_device() != index:
                 _refuse(_DEVICE, f"norm {name}: on {w.device}, the cache is on {device}")
+        self._fits = (index, heads, kv_heads, dim)
 
 
 class SharedPrefix:
@@ -115,12 +119,15 @@ class MxCache(PagedCache):
         are whose) is token start[b] + i (start [seqs] i32; None: the length, so what append() wrote for the step's rows).
         out: a pair of tensors to write to; rows of tokens that the cache does not have are left as they were."""
         width = self.kv_heads * self.dim
-        if out is None:
-            out = tuple(torch.empty((rows, width), dtype=self.dtype, device=self.device) for _ in range(2))
         sp = self._vector("row_start", row_start, torch.int32, self.seqs + 1)
         tp = None if start is None else self._vector("start", start, torch.int32, self.seqs)
-        kp, ks = self._matrix("out k", out[0], self.dtype, rows, width)
-        vp, vs = self._matrix("out v", out[1], self.dtype, rows, width)
+        if out is None:
+            k, v = out = (torch.empty((rows, width), dtype=self.dtype, device=self.device),
+                          torch.empty((rows, width), dtype=self.dtype, device=self.device))
+            kp, vp, ks, vs = k.data_ptr(), v.data_ptr(), width, width
+        else:
+            kp, ks = self._matrix("out k", out[0], self.dtype, rows, width)
+            vp, vs = self._matrix("out v", out[1], self.dtype, rows, width)
         self._launch(_LIB.moe_mx_read, self._ref, rows, sp, tp, kp, ks, vp, vs)
         return out
 
