@@ -54,8 +54,8 @@ enum moe_mx_format {
 /* A paged key/value cache in blocks of 32 values along a head: codes, and a byte e for each block, whose values are code *
  * 2^(e - 127) (e = 255: the block is NaN). Written with the smallest power of two, 2^-126 at least, under which the block's
  * largest magnitude does not pass the largest code, each value rounded once from fp32, to nearest even; a block that holds
- * an infinity or a NaN becomes NaN. With f16 rows the powers stop at 2^7 (MX8) or 2^13 (MX4), and larger values
- * take the largest code, so that what is read back is finite.
+ * an infinity or a NaN becomes NaN. The powers stop where the largest code is finite in the rows' type (2^119 and 2^125 in
+ * bf16, 2^7 and 2^13 in f16), and larger values take the largest code, so that what is read back is finite.
  *   k, v              [pages][page][kv_heads][bytes of a head: dim, or dim / 2] bytes (dtype U8), last dim contiguous, other strides
  *                     multiples of 16, 16-byte aligned; page as in moe_paged_cache; dim 32, 64, 96, 128, 192 or 256
  *   k_scale, v_scale  [pages][page][kv_heads][dim / 32] bytes, last dim contiguous

@@ -1,4 +1,6 @@
 // moe_serving_api.hip -- host side of the C ABI declared in include/moe_serving.h: argument checks, launches.
+#include <utility>
+
 #include "api_checks.h"
 
 namespace moe {
@@ -19,7 +21,21 @@ using namespace moe;
 static int check_bytes(const char *name, const moe_tensor &t, int unit, int align) {
     if (!t.data) return api_fail(MOE_ERR_MISSING_TENSOR, "%s: missing (data == NULL)", name);
     if (t.dtype != MOE_DT_U8) return api_fail(MOE_ERR_DTYPE, "%s: dtype %s, expected u8", name, type_name(t.dtype));
-    return check_paged(name, t, unit, align);
+    const int rc = check_paged(name, t, unit, align);
+    if (rc) return rc;
+    // no two elements in one place: each dim's stride past all that the dims of lesser strides reach
+    int order[3] = {0, 1, 2};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 3; ++j)
+            if (t.stride[order[j]] < t.stride[order[i]]) std::swap(order[i], order[j]);
+    int64_t reach = t.shape[3];
+    for (const int i : order) {
+        if (t.shape[i] == 1) continue;
+        if (t.stride[i] < reach)
+            return api_fail(MOE_ERR_LAYOUT, "%s: stride[%d] = %lld: elements overlap", name, i, (long long)t.stride[i]);
+        reach += (t.shape[i] - 1) * t.stride[i];
+    }
+    return MOE_OK;
 }
 
 static int check_mx(const moe_mx_cache *c, CacheParams &p) {

@@ -42,15 +42,16 @@ template <bool F16, int FMT> __device__ __forceinline__ void mx_expand(const u32
 }
 
 // The scale byte of a block whose largest magnitude is `top`: of the smallest power of two, 2^-126 at least, under which it
-// does not pass the largest code (448 or 6); 255 where it is not finite. In f16 the power stops where the
-// largest code reaches the last finite numbers (2^7, 2^13), and what is larger takes the largest code.
+// does not pass the largest code (448 or 6); 255 where it is not finite. The power stops where the largest code is still
+// finite in the rows' type (2^119 and 2^125 in bf16, 2^7 and 2^13 in f16), and what is larger takes the largest code.
+template <bool F16, int FMT> constexpr uint32_t mx_last_scale() { return (F16 ? 142 : 254) - (FMT == MX_E4M3 ? 8 : 2); }
 template <bool F16, int FMT> __device__ __forceinline__ uint32_t mx_scale(float top) {
     constexpr int EMAX = FMT == MX_E4M3 ? 8 : 2;                              // exponent of the largest code
     constexpr uint32_t FRACTION = FMT == MX_E4M3 ? 0x600000u : 0x400000u;     // and its fraction, 1.75 and 1.5
     const uint32_t bits = __float_as_uint(top) & 0x7FFFFFFFu;
     if (bits >= 0x7F800000u) return 255;
     const int e = (int)(bits >> 23) - EMAX + ((bits & 0x7FFFFFu) > FRACTION ? 1 : 0);
-    return (uint32_t)min(max(e, 1), F16 ? 142 - EMAX : 254);
+    return (uint32_t)min(max(e, 1), (int)mx_last_scale<F16, FMT>());
 }
 
 // Eight values of a block with scale byte e as codes, to nearest even: 8 bytes, or 4 in the first word.

@@ -166,10 +166,11 @@ template <typename L> __global__ void __launch_bounds__(256) moe_sample_cells_ke
     const int64_t at = (int64_t)row * p.chunks + c;
     const double top_g = grid(top, h.steps);
     // Two kinds of chunks are taken slowly, and not listed: with an infinite logit, or a temperature next to 0 (places that 32 bits
-    // do not hold); with many equal logits (a wave's first ones), whose additions at one place would take one after another
+    // do not hold) or so large that no number is low enough to weigh nothing; with many equal logits (a wave's first ones), whose
+    // additions at one place would take one after another
     const float lowest = (float)((top_g - 2304.0) / h.steps);      // what lies below weighs nothing
     const bool equal = x[0] > lowest && __ballot(x[0] == __int_as_float(uniform(__float_as_int(x[0])))) == ~0ull;
-    const bool slow = __syncthreads_or(equal || !(fabs(top_g) < 0x1p29)) != 0;
+    const bool slow = __syncthreads_or(equal || !(fabs(top_g) < 0x1p29 && lowest > -__builtin_inff())) != 0;
     if (tid == 0) p.head[at] = {top_g, top, !slow};
     if (!(top > -__builtin_inff())) return;
     if (slow) {
@@ -723,7 +724,7 @@ template <typename L> __global__ void __launch_bounds__(ROW_THREADS) moe_sample_
             if (i == M) {
                 // the logarithm in 32 bits is within 1/100 of a step
                 const double g = top_g + (double)(32.0f * __log2f((float)least_weight));
-                c = {cells_below(top_g, g + 0.75), cells_below(top_g, g - 0.75)};
+                c = {max(cells_below(top_g, g + 0.75), 0), cells_below(top_g, g - 0.75)};
                 if (top_g == __builtin_inf()) c = {0, 0};
             } else {
 #pragma unroll 1

@@ -231,7 +231,7 @@ template <bool F16, int FMT, int MOST> __global__ void __launch_bounds__(MOST, M
                 dst = (uint8_t *)p.c.v.p + v_at + h * p.c.v.head;
                 scales = (uint8_t *)p.c.vs.p + page * p.c.vs.page + slot * p.c.vs.slot + h * p.c.vs.head;
             }
-            if (F16 && scale != 255) {
+            if (scale == mx_last_scale<F16, FMT>()) {
                 const float most = __uint_as_float(scale << 23) * (FMT == MX_E4M3 ? 448.0f : 6.0f);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = fminf(fmaxf(x[e], -most), most);

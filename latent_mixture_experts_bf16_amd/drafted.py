@@ -203,8 +203,8 @@ class PagedCache(_Caller):
             _refuse(_SHAPE, f"{name}: {width} wide, not heads of {self.dim}")
         return rows, width // self.dim
 
-    # the calls of a cache of codes differ in these (serving.MxCache)
-    _append_call, _keep_call = _LIB.moe_norm_rope_append, _LIB.moe_path_keep
+    # the calls of a cache of codes differ in these (serving.MxCache); without a norm there is a plain one here
+    _append_call, _keep_call, _plain_append = _LIB.moe_norm_rope_append, _LIB.moe_path_keep, True
 
     def append(self, rope: Rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, row_start: torch.Tensor,
                positions: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
@@ -227,7 +227,7 @@ class PagedCache(_Caller):
         if out is None:
             out = torch.empty((rows, heads * self.dim), dtype=self.dtype, device=self.device)
         op, os_ = self._matrix("out", out, self.dtype, rows, heads * self.dim)
-        if norm is None and type(self) is PagedCache:
+        if norm is None and self._plain_append:
             self._launch(_LIB.moe_rope_append, self._ref, rope._ref, rows, qp, qs, heads, kp, ks, vp, vs, sp, pp, op, os_)
             return out
         np_ = None

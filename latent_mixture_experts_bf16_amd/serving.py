@@ -95,7 +95,7 @@ class MxCache(PagedCache):
     tensors that the caller owns (mx_cache() lays them out as they are read fastest); dim 32, 64, 96, 128, 192 or 256. dtype: of the
     rows that are appended, of queries and results, and what codes are read as."""
 
-    _append_call, _keep_call = _LIB.moe_mx_append, _LIB.moe_mx_keep
+    _append_call, _keep_call, _plain_append = _LIB.moe_mx_append, _LIB.moe_mx_keep, False
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, table: torch.Tensor,
                  length: torch.Tensor, format: str = "mx8", dtype: torch.dtype = torch.bfloat16):
