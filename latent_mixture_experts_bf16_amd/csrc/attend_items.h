@@ -114,6 +114,13 @@ struct EntryWork {
     int64_t units;
 };
 
+// The number of the first item of an entry whose rows begin with `first`, of a head: items of a batch that shares prompts have
+// numbers that rise in the order of work, entry by entry and head by head. Entries' rows follow one another and the last tile
+// of each may be part empty, so these number up to rows * group / tile + entries, and an entry's items end before the next one's.
+__device__ __forceinline__ int64_t item_number(int first, int group, int tile, int entry, int kv_heads) {
+    return ((int64_t)first * group / tile + entry) * kv_heads;
+}
+
 // Tokens of group g's shared prompt that are computed for all: whole tiles of it.
 __device__ __forceinline__ int shared_tokens(const AttendParams &p, int g) {
     return min(max(p.shared_len[g], 0), p.c.cap) & ~63;
@@ -145,7 +152,7 @@ template <int MQ, bool SHARED> __device__ __forceinline__ EntryWork entry_work(c
     w.len = t < 0 ? 0 : min(t, p.c.cap);
     const bool past = w.len + (int64_t)w.n > p.c.cap;
     w.end = past ? p.c.cap : w.len + w.n;
-    if (SHARED) w.skip = p.skip ? p.skip[b] >> 6 : 0;
+    if (SHARED) w.skip = p.shares ? p.shares[b].skip >> 6 : 0;
     w.mts = (int)(((int64_t)w.n * p.group + MQ - 1) / MQ);
     w.tts = max(0, (int)(((int64_t)w.end + 63) >> 6) - w.skip);
     w.units = (int64_t)w.mts * (w.tts + ITEM_COST) * p.c.heads;
@@ -157,7 +164,7 @@ template <int MQ, bool SHARED> __device__ __forceinline__ EntryWork entry_work(c
 }
 
 // In the first launch over a shared prompt, for the second: how many tokens of each sequence (whole tiles) its group's pass
-// has taken. A sequence keeps one tile at least for itself, in which its own rows lie. By the threads of one workgroup.
+// has taken, and the group. A sequence keeps one tile at least for itself, in which its own rows lie. By the threads of one workgroup.
 __device__ __forceinline__ void tell_skips(const AttendParams &p) {
     for (int b = (int)threadIdx.x; b < p.c.seqs; b += 256) {
         int lo = 0, hi = p.groups;            // the last group that starts at or before b
@@ -171,7 +178,9 @@ __device__ __forceinline__ void tell_skips(const AttendParams &p) {
         if (group_bad) raise_flag(p.c.flags, MOE_FLAG_GROUPS);
         if (shared < 0 || shared > len) raise_flag(p.c.flags, MOE_FLAG_LEN);
         const int64_t end = min((int64_t)p.c.cap, (int64_t)max(len, 0) + max(0, e - s));
-        p.skip_out[b] = group_bad || end < 1 ? 0 : min(shared_tokens(p, lo), (int)((end - 1) & ~63ll));
+        const int skip = group_bad || end < 1 ? 0 : min(shared_tokens(p, lo), (int)((end - 1) & ~63ll));
+        const int first = skip ? p.row_start[from] : 0, behind = skip ? p.row_start[to] : 0;
+        p.tell[b] = {first < 0 || behind > p.rows ? 0 : skip, lo, first, behind};
     }
     if (threadIdx.x == 0 && (p.group_start[0] != 0 || p.group_start[p.groups] != p.c.seqs))
         raise_flag(p.c.flags, MOE_FLAG_GROUPS);
@@ -239,8 +248,8 @@ __device__ __forceinline__ bool find_range(const AttendParams &p, PlanLds &s, in
 }
 
 // FMT: the cache's format (MX_NONE: the 16-bit type of the queries). SHARED: the kernel can be either launch of a batch that
-// shares a prompt. The first (p.group_start) takes the prompt's tokens for all rows of a group and leaves each query's
-// maximum, sum and weighted values; the second starts from them and skips those tokens.
+// shares a prompt. The first (p.group_start) takes the prompt's tokens for all rows of a group, the second skips them; both leave
+// parts, which a launch of their own joins.
 template <bool F16, int D, int NQ, int QW, int FMT, bool SHARED>
 __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_attend_kernel(AttendParams p) {
     constexpr int MQ = 16 * NQ * QW, TG = 4 / QW, NS = QW;     // a wave's 16-token groups in a tile: 4 / TG
@@ -338,14 +347,6 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
             l[u] = 0.0f;
 #pragma unroll
             for (int d = 0; d < DB; ++d) o[u][d] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (SHARED && skip && t_from == 0 && wt == 0 && ok) {      // what the shared prompt's tokens summed to
-                const int64_t at = (int64_t)(first + i) * p.q_heads + h * p.group + g;
-                const float2 ml = *(const float2 *)(p.prior_stat + at * 2);
-                m[u] = ml.x;
-                l[u] = quad == 0 ? ml.y : 0.0f;
-#pragma unroll
-                for (int d = 0; d < DB; ++d) o[u][d] = *(const f32x4 *)(p.prior_sum + at * D + d * 16 + quad * 4);
-            }
         }
         // whether the query of this lane's column sees token t (without branches)
         auto sees = [&](int u, int t) {
@@ -565,9 +566,14 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
                 *(f32x4 *)(stage + (wave * 16 * NQ + q) * D + ((d * 4 + quad) ^ (q & (PU - 1))) * 4) = o[u][d];
         }
         __syncthreads();
-        const bool whole = t_from == 0 && t_to == tts;
-        const int slot = 2 * w + (t_from == 0 ? 1 : 0);
-        float *const pm = p.part_stat + (int64_t)slot * 2 * MQ, *const po = p.part_sum + (int64_t)slot * MQ * D;
+        const bool shares = SHARED && p.items;
+        // of a batch that shares prompts every item is a part: its query's other parts come from the other launch
+        const bool whole = t_from == 0 && t_to == tts && !shares;
+        // An item's parts lie one after another: where all are parts, the one of item i in range w in slot i + w, which rises by
+        // one at least from part to part.
+        const int64_t number = shares ? item_number(first, p.group, MQ, b, p.c.heads) + item : 0;
+        const int64_t slot = shares ? number + w : 2 * w + (t_from == 0 ? 1 : 0);
+        float *const pm = p.part_stat + slot * 2 * MQ, *const po = p.part_sum + slot * MQ * D;
         for (int at = tid; at < queries * (D / 8); at += 256) {
             const int q = at / (D / 8), d8 = at % (D / 8), ql = q % (16 * NQ), wv = q / (16 * NQ);
             float top = sm[wv][ql];
@@ -585,13 +591,8 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
                 lo += f * *(const f32x4 *)(src + ((2 * d8) ^ (ql & (PU - 1))) * 4);
                 hi += f * *(const f32x4 *)(src + ((2 * d8 + 1) ^ (ql & (PU - 1))) * 4);
             }
-            const int z = mt * MQ + q, i = z / p.group, g = z - i * p.group;
-            if (SHARED && whole && p.group_start) {
-                const int64_t at = (int64_t)(first + i) * p.q_heads + h * p.group + g;
-                if (d8 == 0) *(float2 *)(p.prior_stat + at * 2) = make_float2(top, sum);
-                *(f32x4 *)(p.prior_sum + at * D + d8 * 8) = lo;
-                *(f32x4 *)(p.prior_sum + at * D + d8 * 8 + 4) = hi;
-            } else if (whole) {
+            if (whole) {
+                const int z = mt * MQ + q, i = z / p.group, g = z - i * p.group;
                 const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
                 const f32x4 a = sum == 0.0f ? f32x4{0.f, 0.f, 0.f, 0.f} : lo * inv;
                 const f32x4 c = sum == 0.0f ? f32x4{0.f, 0.f, 0.f, 0.f} : hi * inv;
@@ -606,11 +607,16 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
         if (!whole && t_from == 0 && tid == 0) {
             // the first part of a cut item: the ranges that hold it are this one and the next ones
             const int64_t last = x - u_to + all_units;
-            part.first = first;
-            part.mt = mt;
-            part.head = h;
-            part.queries = queries;
-            part.count = (int)min(divide(last * groups - 1, total), groups - 1) - w + 1;
+            const int count = (int)min(divide(last * groups - 1, total), groups - 1) - w + 1;
+            if (shares) {
+                p.items[number] = {w, t_to == tts ? 1 : count};
+            } else {
+                part.first = first;
+                part.mt = mt;
+                part.head = h;
+                part.queries = queries;
+                part.count = count;
+            }
         }
         __syncthreads();
     }
@@ -738,21 +744,127 @@ __global__ void __launch_bounds__(256) moe_attend_join_kernel(AttendParams p) {
         } else {
             j = join_parts<D>(p, w, q, 0, part.count);
         }
-        const float best_of = shared ? fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3])) : j.top;
-        const int z = part.mt * p.tile_queries + q, row = z / p.group, g = z - row * p.group;
-        if (p.group_start) {           // of a shared prompt: left for the second launch
-            if (lane < U && (!shared || wave == 0)) {
-                const int64_t to = (int64_t)(part.first + row) * p.q_heads + part.head * p.group + g;
-                if (lane == 0) *(float2 *)(p.prior_stat + to * 2) = make_float2(best_of, j.sum);
-                *(f32x4 *)(p.prior_sum + to * D + lane * 4) = j.o;
-            }
-        } else if (lane < U && (!shared || wave == 0)) {
+        if (lane < U && (!shared || wave == 0)) {
+            const int z = part.mt * p.tile_queries + q, row = z / p.group, g = z - row * p.group;
             const float inv = 1.0f / j.sum;
             const f32x4 r = j.sum == 0.0f ? f32x4{0.f, 0.f, 0.f, 0.f} : j.o * inv;
             *(uint2 *)(p.out + (int64_t)(part.first + row) * p.out_stride + (int64_t)(part.head * p.group + g) * D + lane * 4) =
                 make_uint2(pack2<F16>(r[0], r[1]), pack2<F16>(r[2], r[3]));
         }
         if (shared) __syncthreads();
+    }
+}
+
+// The sums of two sets of tokens as one.
+__device__ __forceinline__ JoinSum join_two(const JoinSum &a, const JoinSum &b) {
+    const float best = fmaxf(a.top, b.top), from = best == -__builtin_inff() ? 0.0f : best;
+    const float fa = __builtin_amdgcn_exp2f(a.top - from), fb = __builtin_amdgcn_exp2f(b.top - from);
+    return {best, a.sum * fa + b.sum * fb, a.o * fa + b.o * fb};
+}
+
+// The parts [lo, hi) of query q, one wave: part a lies in slot at + a. The lanes lie along the head (D / 4 of them) and along the
+// parts, four steps on their way at once. The answer is that of all parts in every lane below D / 4.
+template <int D> __device__ __forceinline__ JoinSum join_slots(const PassParts &pass, int64_t at, int q, int lo, int hi) {
+    constexpr int U = D / 4, PL = 64 / U, STEPS = 4;
+    const int lane = lane_id(), k = lane / U, u = lane % U, MQ = pass.tile_queries;
+    JoinSum j = {-__builtin_inff(), 0.0f, {0.f, 0.f, 0.f, 0.f}};
+    for (int a0 = lo; a0 < hi; a0 += STEPS * PL) {
+        float m[STEPS], s[STEPS];
+        f32x4 v[STEPS];
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            const int a = a0 + i * PL + k;
+            m[i] = -__builtin_inff();
+            s[i] = 0.0f;
+            v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (k < PL && a < hi) {
+                const float *const stat = pass.stat + (at + a) * 2 * MQ + q;
+                m[i] = stat[0];
+                s[i] = stat[MQ];
+                v[i] = *(const f32x4 *)(pass.sum + ((at + a) * MQ + q) * D + u * 4);
+            }
+        }
+        float best = j.top;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) best = fmaxf(best, m[i]);
+        const float from = best == -__builtin_inff() ? 0.0f : best, old = __builtin_amdgcn_exp2f(j.top - from);
+        j.sum *= old;
+        j.o *= old;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            const float f = __builtin_amdgcn_exp2f(m[i] - from);
+            j.sum += f * s[i];
+            j.o += f * v[i];
+        }
+        j.top = best;
+    }
+    JoinSum all = j;
+#pragma unroll
+    for (int i = 1; i < PL; ++i) {
+        JoinSum next;
+        next.top = __shfl(j.top, i * U + u);
+        next.sum = __shfl(j.sum, i * U + u);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) next.o[e] = __shfl(j.o[e], i * U + u);
+        all = join_two(all, next);
+    }
+    return all;
+}
+
+// Joins the parts of a batch that shares prompts: of each query those of its group's prompt and those of its own sequence. A
+// workgroup takes one query where they are few, three waves a third of its prompt's parts each; else a wave one. What bounds it is
+// a chain of loads, each at an address that the one before gave: the row's sequence, its group, the item, the parts. 64
+// registers, so that a CU holds eight workgroups, and few steps in that chain: 2048 queries of some 16 parts each 10.3 us (with
+// parts' maxima read before their sums, in 136 registers, 15.8; a launch for each pass' parts, before, 16 and a gap).
+template <bool F16, int D>
+__global__ void __launch_bounds__(256, 8) moe_shared_join_kernel(SharedJoinParams p) {
+    constexpr int U = D / 4;
+    __shared__ float sm[4], ss[4];
+    __shared__ f32x4 so[4][U];
+    const int lane = lane_id(), wave = uniform((int)threadIdx.x >> 6);
+    const bool apart = p.apart != 0;       // a workgroup for each query
+    const int64_t query = apart ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
+    const int row = uniform((int)divide(query, p.q_heads)), head = uniform((int)(query - (int64_t)row * p.q_heads));
+    if (row >= p.rows) return;
+    int first = 0;
+    const int b = seq_of_row(p.row_start, p.seqs, row, &first);
+    if (b < 0) return;                     // reported by the launches before, as are the rows past the last
+    const int behind = uniform(p.row_start[b + 1]);
+    const int4 s = *(const int4 *)(p.shares + b);
+    const SequenceShare share = {uniform(s.x), uniform(s.y), uniform(s.z), uniform(s.w)};
+    if (behind > p.rows) return;
+    const int h = head / p.group, g = head - h * p.group;
+    // parts [from, to) of the thirds of an item's parts, of query q of an entry with rows [first, behind). The record of the
+    // item is held to the ranges that there are.
+    auto join = [&](const PassParts &pass, int entry, int first, int behind, int from, int to) {
+        const int z = (row - first) * p.group + g, mt = z / pass.tile_queries;
+        const int mts = (int)(((int64_t)(behind - first) * p.group + pass.tile_queries - 1) / pass.tile_queries);
+        const int64_t number = item_number(first, p.group, pass.tile_queries, entry, p.kv_heads) + (int64_t)h * mts + mt;
+        const int2 r = *(const int2 *)(pass.items + number);
+        const int w = min(max(uniform(r.x), 0), pass.ranges - 1), count = min(uniform(r.y), pass.ranges - w), each = (count + 2) / 3;
+        return join_slots<D>(pass, number + w, z - mt * pass.tile_queries, min(count, from * each), min(count, to * each));
+    };
+    // where waves share a query the last has the query's own parts, the others thirds of its group's
+    JoinSum j = {-__builtin_inff(), 0.0f, {0.f, 0.f, 0.f, 0.f}};
+    if (!apart || wave == 3) j = join(p.own, b, first, behind, 0, 3);
+    if (share.skip && share.first <= row && row < share.behind && !(apart && wave == 3)) {
+        const JoinSum k = join(p.common, share.group, share.first, share.behind, apart ? wave : 0, apart ? wave + 1 : 3);
+        j = join_two(j, k);
+    }
+    if (apart) {
+        if (lane < U) so[wave][lane] = j.o;
+        if (lane == 0) { sm[wave] = j.top; ss[wave] = j.sum; }
+        __syncthreads();
+        if (wave) return;
+        if (lane < U)
+#pragma unroll
+            for (int k = 1; k < 4; ++k) j = join_two(j, {sm[k], ss[k], so[k][lane]});
+    }
+    if (lane < U) {
+        const float inv = 1.0f / j.sum;
+        const f32x4 r = j.sum == 0.0f ? f32x4{0.f, 0.f, 0.f, 0.f} : j.o * inv;
+        *(uint2 *)(p.out + (int64_t)row * p.out_stride + (int64_t)head * D + lane * 4) =
+            make_uint2(pack2<F16>(r[0], r[1]), pack2<F16>(r[2], r[3]));
     }
 }
 

@@ -1,5 +1,5 @@
-// attend_kernels.hip -- the attention kernels of a cache in the queries' own 16-bit type (gfx950), and the launch that joins
-// parts, which is the same for every format.
+// attend_kernels.hip -- the attention kernels of a cache in the queries' own 16-bit type (gfx950), and the launches that join
+// parts, which are the same for every format.
 #include "attend_items.h"
 
 namespace moe {
@@ -14,7 +14,9 @@ namespace moe {
     template __global__ void moe_attend_kernel<true, D, 2, 2, MX_NONE, false>(AttendParams);  \
     template __global__ void moe_attend_kernel<true, D, 2, 4, MX_NONE, false>(AttendParams);  \
     template __global__ void moe_attend_join_kernel<false, D>(AttendParams);              \
-    template __global__ void moe_attend_join_kernel<true, D>(AttendParams)
+    template __global__ void moe_attend_join_kernel<true, D>(AttendParams);               \
+    template __global__ void moe_shared_join_kernel<false, D>(SharedJoinParams);          \
+    template __global__ void moe_shared_join_kernel<true, D>(SharedJoinParams)
 ATTEND_KERNELS(32);
 ATTEND_KERNELS(64);
 ATTEND_KERNELS(80);

@@ -5,8 +5,15 @@
 namespace moe {
 template <bool F16, int D, int NQ, int QW, int FMT, bool SHARED> __global__ void moe_attend_kernel(AttendParams p);
 template <bool F16, int D> __global__ void moe_attend_join_kernel(AttendParams p);
+template <bool F16, int D> __global__ void moe_shared_join_kernel(SharedJoinParams p);
 
 typedef void (*AttendKernel)(AttendParams);
+typedef void (*SharedJoin)(SharedJoinParams);
+
+struct Kernels {
+    AttendKernel main, join;
+    SharedJoin shared_join;
+};
 
 template <bool F16, int D, int FMT, bool SHARED> static AttendKernel of_tile(int queries) {
     return queries == 16   ? moe_attend_kernel<F16, D, 1, 1, FMT, SHARED>
@@ -21,12 +28,13 @@ template <bool F16, int D> static AttendKernel of_format(int format, bool groups
     }
     return groups ? of_tile<F16, D, MX_NONE, true>(queries) : of_tile<F16, D, MX_NONE, false>(queries);
 }
-template <bool F16> static void of_dim(int dim, int format, bool groups, int queries, AttendKernel *main, AttendKernel *join) {
+template <bool F16> static void of_dim(int dim, int format, bool groups, int queries, Kernels *k) {
     switch (dim) {
 #define ATTEND_DIM(D)                                      \
     case D:                                                \
-        *main = of_format<F16, D>(format, groups, queries); \
-        *join = moe_attend_join_kernel<F16, D>;            \
+        k->main = of_format<F16, D>(format, groups, queries); \
+        k->join = moe_attend_join_kernel<F16, D>;          \
+        k->shared_join = moe_shared_join_kernel<F16, D>;   \
         break
         ATTEND_DIM(32);
         ATTEND_DIM(64);
@@ -44,10 +52,11 @@ template <bool F16> static void of_dim(int dim, int format, bool groups, int que
 // work; and the workspace's layout.
 struct AttendShape {
     int queries, ranges;
-    int64_t stat, sum, bytes;
+    int64_t items, stat, sum, bytes;
 };
-// entries: the sequences, or the groups of them that a shared prompt's tokens are computed for together.
-static AttendShape attend_shape(const CacheParams &c, int32_t rows, int32_t q_heads, int32_t entries) {
+// entries: the sequences, or the groups of them that a shared prompt's tokens are computed for together. shares: of a batch that
+// shares prompts, whose items are all parts.
+static AttendShape attend_shape(const CacheParams &c, int32_t rows, int32_t q_heads, int32_t entries, bool shares) {
     AttendShape s;
     // The least tile that holds the queries that share a key head, on average over the entries (their
     // own numbers are on the device): a sequence with more of them reads its cache again. (8 trees of 8 to 16 rows, 4
@@ -55,49 +64,51 @@ static AttendShape attend_shape(const CacheParams &c, int32_t rows, int32_t q_he
     const int64_t mean = ((int64_t)rows * (q_heads / c.heads) + entries - 1) / entries;
     s.queries = mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128;
     s.ranges = COMPUTE_UNITS * attend_blocks(c.dim, s.queries);     // as many workgroups as the card holds at once
+    // at most two parts a range; and where all are, a number for each item and a range's number more
+    s.items = shares ? ((int64_t)rows * (q_heads / c.heads) / s.queries + entries) * c.heads : 0;
+    const int64_t parts = shares ? s.items + s.ranges : 2 * s.ranges;
     s.stat = (int64_t)s.ranges * sizeof(AttendPart);
-    s.sum = s.stat + (int64_t)s.ranges * 2 * 2 * s.queries * 4;
-    s.bytes = s.sum + (int64_t)s.ranges * 2 * s.queries * c.dim * 4;
+    s.sum = s.stat + parts * 2 * s.queries * 4;
+    s.bytes = s.sum + parts * s.queries * c.dim * 4;
     return s;
 }
 
-// What a shared prompt's pass leaves for the second one, behind the parts: tokens taken of each sequence, statistics, sums.
-struct PriorShape {
-    int64_t skip, stat, sum, bytes;
+static int64_t aligned(int64_t n) { return (n + 15) & ~15ll; }
+
+// The workspace of a batch that shares prompts: the parts and items of both launches, and of each sequence its group and the tokens
+// that are taken for it.
+struct SharedShape {
+    AttendShape common, own;
+    int64_t own_at, common_items, own_items, shares, bytes;
 };
-static PriorShape prior_shape(const CacheParams &c, int32_t rows, int32_t q_heads, int64_t parts) {
-    PriorShape s;
-    s.skip = (parts + 15) & ~15ll;
-    s.stat = (s.skip + (int64_t)c.seqs * 4 + 15) & ~15ll;
-    s.sum = (s.stat + (int64_t)rows * q_heads * 8 + 15) & ~15ll;
-    s.bytes = s.sum + (int64_t)rows * q_heads * c.dim * 4;
+static SharedShape shared_shape(const CacheParams &c, int32_t rows, int32_t q_heads, int32_t groups) {
+    SharedShape s;
+    s.common = attend_shape(c, rows, q_heads, groups, true);
+    s.own = attend_shape(c, rows, q_heads, c.seqs, true);
+    s.own_at = aligned(s.common.bytes);
+    s.common_items = s.own_at + aligned(s.own.bytes);
+    s.own_items = s.common_items + aligned(s.common.items * sizeof(AttendItem));
+    s.shares = s.own_items + aligned(s.own.items * sizeof(AttendItem));
+    s.bytes = s.shares + (int64_t)c.seqs * sizeof(SequenceShare);
     return s;
 }
 
 int64_t attend_workspace(const CacheParams &c, int32_t rows, int32_t q_heads, int32_t groups) {
-    const int64_t own = attend_shape(c, rows, q_heads, c.seqs).bytes;
-    if (!groups) return own;
-    const int64_t common = attend_shape(c, rows, q_heads, groups).bytes;
-    return prior_shape(c, rows, q_heads, own > common ? own : common).bytes;
+    return groups ? shared_shape(c, rows, q_heads, groups).bytes : attend_shape(c, rows, q_heads, c.seqs, false).bytes;
 }
 
-static int launch_pass(const AttendCall &a, AttendParams &p, const AttendShape &shape) {
+// The launch of a pass whose parts lie at `base`.
+static int launch_pass(const AttendCall &a, AttendParams &p, const AttendShape &shape, char *base, Kernels *k) {
     p.tile_queries = shape.queries;
     p.ranges = shape.ranges;
-    p.parts = (AttendPart *)a.workspace;
-    p.part_stat = (float *)((char *)a.workspace + shape.stat);
-    p.part_sum = (float *)((char *)a.workspace + shape.sum);
-    AttendKernel main, join;
+    p.parts = (AttendPart *)base;
+    p.part_stat = (float *)(base + shape.stat);
+    p.part_sum = (float *)(base + shape.sum);
     if (a.f16)
-        of_dim<true>(p.c.dim, a.format, a.shared != nullptr, shape.queries, &main, &join);
+        of_dim<true>(p.c.dim, a.format, a.shared != nullptr, shape.queries, k);
     else
-        of_dim<false>(p.c.dim, a.format, a.shared != nullptr, shape.queries, &main, &join);
-    int rc;
-    if ((rc = launch("attend", main, dim3((unsigned)shape.ranges), dim3(256), p, a.stream))) return rc;
-    // More workgroups join more queries at once, but each lists the work first: few queries a key head make few
-    // (item, query) pairs (one row over 777 tokens: 5.9 us with 512, 6.4 with 1024), many make thousands (64-row trees
-    // over 4100: 14.7 and 10.3).
-    return launch("attend join", join, dim3(shape.queries == 16 ? 512 : 1024), dim3(256), p, a.stream);
+        of_dim<false>(p.c.dim, a.format, a.shared != nullptr, shape.queries, k);
+    return launch("attend", k->main, dim3((unsigned)shape.ranges), dim3(256), p, a.stream);
 }
 
 int check_shared(const moe_shared_prefix *s, const CacheParams &c) {
@@ -120,7 +131,6 @@ int attend_run(const AttendCall &a, AttendParams &p) {
     if (rows_overlap(a.out, a.out_stride, w, a.q, a.q_stride, w, a.rows))
         return api_fail(MOE_ERR_ALIAS, "out overlaps q");
     if (a.shared && (rc = check_shared(a.shared, p.c))) return rc;
-    const AttendShape own = attend_shape(p.c, a.rows, a.q_heads, p.c.seqs);
     const int32_t groups = a.shared ? a.shared->groups : 0;
     if ((rc = check_workspace(a.workspace, a.workspace_bytes, attend_workspace(p.c, a.rows, a.q_heads, groups))) ||
         (rc = check_device()))
@@ -137,24 +147,51 @@ int attend_run(const AttendCall &a, AttendParams &p) {
     p.rows = a.rows;
     p.q_heads = a.q_heads;
     p.group = a.q_heads / p.c.heads;
-    if (a.shared) {
-        const AttendShape common = attend_shape(p.c, a.rows, a.q_heads, groups);
-        const PriorShape prior = prior_shape(p.c, a.rows, a.q_heads, own.bytes > common.bytes ? own.bytes : common.bytes);
-        int32_t *skip = (int32_t *)((char *)a.workspace + prior.skip);
-        p.prior_stat = (float *)((char *)a.workspace + prior.stat);
-        p.prior_sum = (float *)((char *)a.workspace + prior.sum);
-        p.entries = p.groups = groups;
-        p.group_start = a.shared->group_start;
-        p.shared_len = a.shared->len;
-        p.skip_out = skip;
-        if ((rc = launch_pass(a, p, common))) return rc;
-        p.group_start = p.shared_len = nullptr;
-        p.skip_out = nullptr;
-        p.skip = skip;
+    char *const base = (char *)a.workspace;
+    Kernels k;
+    if (!a.shared) {
+        const AttendShape own = attend_shape(p.c, a.rows, a.q_heads, p.c.seqs, false);
+        p.entries = p.c.seqs;
+        p.mask = a.mask;
+        if ((rc = launch_pass(a, p, own, base, &k))) return rc;
+        // More workgroups join more queries at once, but each lists the work first: few queries a key head make few
+        // (item, query) pairs (one row over 777 tokens: 5.9 us with 512, 6.4 with 1024), many make thousands (64-row trees
+        // over 4100: 14.7 and 10.3).
+        return launch("attend join", k.join, dim3(own.queries == 16 ? 512 : 1024), dim3(256), p, a.stream);
     }
+    const SharedShape s = shared_shape(p.c, a.rows, a.q_heads, groups);
+    SharedJoinParams j;
+    memset(&j, 0, sizeof j);
+    p.entries = p.groups = groups;
+    p.group_start = a.shared->group_start;
+    p.shared_len = a.shared->len;
+    p.tell = (SequenceShare *)(base + s.shares);
+    p.items = (AttendItem *)(base + s.common_items);
+    if ((rc = launch_pass(a, p, s.common, base, &k))) return rc;
+    j.common = {p.items, p.part_stat, p.part_sum, p.tile_queries, p.ranges};
     p.entries = p.c.seqs;
+    p.group_start = p.shared_len = nullptr;
+    p.shares = p.tell;
+    p.tell = nullptr;
     p.mask = a.mask;
-    return launch_pass(a, p, own);
+    p.items = (AttendItem *)(base + s.own_items);
+    if ((rc = launch_pass(a, p, s.own, base + s.own_at, &k))) return rc;
+    j.own = {p.items, p.part_stat, p.part_sum, p.tile_queries, p.ranges};
+    j.row_start = a.row_start;
+    j.shares = p.shares;
+    j.out = p.out;
+    j.out_stride = p.out_stride;
+    j.rows = p.rows;
+    j.q_heads = p.q_heads;
+    j.kv_heads = p.c.heads;
+    j.group = p.group;
+    j.seqs = p.c.seqs;
+    // A workgroup for each query while all run at once (512 queries of 16 rows after 16000 tokens: the call 44.7 us, 47.8 with a
+    // wave for each; 128 queries: 20.7 and 22.4; 2048: the same); past that its other waves and its barrier cost more than
+    // they save (4096: 109 and 106 us; 8192 of 256 short sequences: 67 and 57).
+    const int64_t queries = (int64_t)p.rows * p.q_heads;
+    j.apart = queries < 8 * COMPUTE_UNITS;
+    return launch("shared join", k.shared_join, dim3((unsigned)(j.apart ? queries : (queries + 3) / 4)), dim3(256), j, a.stream);
 }
 
 }  // namespace moe

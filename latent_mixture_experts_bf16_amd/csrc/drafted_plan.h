@@ -101,14 +101,40 @@ struct AttendParams {
     AttendPart *parts;          // [ranges]
     float *part_stat;           // [2 ranges][2][tile_queries]: maximum, sum
     float *part_sum;            // [2 ranges][tile_queries][dim]
-    // a batch that shares prompts: entries of work (groups, then sequences), what its first launch is told, and what it
-    // leaves for the second
+    // a batch that shares prompts: entries of work (groups, then sequences), what its first launch is told, and what the
+    // launches leave for the one that joins their parts
     int32_t entries, groups;
     const int32_t *group_start, *shared_len;    // NULL in the second launch
-    int32_t *skip_out;
-    const int32_t *skip;        // [seqs], NULL in the first launch
-    float *prior_stat;          // [rows][q_heads][2]: maximum, sum
-    float *prior_sum;           // [rows][q_heads][dim]
+    struct SequenceShare *tell;                 // [seqs], NULL in the second launch
+    const struct SequenceShare *shares;         // the same, NULL in the first
+    struct AttendItem *items;   // by items' numbers
+};
+
+// What the first launch takes of a sequence: tokens, whose group, which has rows [first, behind).
+struct alignas(16) SequenceShare {
+    int32_t skip, group, first, behind;
+};
+
+// The first range that holds a part of an item, and how many do.
+struct alignas(8) AttendItem {
+    int32_t w, count;
+};
+
+// What one launch left.
+struct PassParts {
+    const AttendItem *items;
+    const float *stat, *sum;
+    int32_t tile_queries, ranges;
+};
+
+struct SharedJoinParams {
+    PassParts common, own;
+    const int32_t *row_start;
+    const SequenceShare *shares;
+    uint16_t *out;
+    int64_t out_stride;
+    int32_t rows, q_heads, kv_heads, group, seqs;
+    int32_t apart;              // a workgroup for each query, not a wave
 };
 
 // A call of the attention operators whose cache is checked and in the parameters (attend_launch.hip checks the rest).

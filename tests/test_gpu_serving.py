@@ -283,6 +283,8 @@ def _share(P, groups, lengths):
     (6, 1, 256, 128, [256, 257], [17, 30], 3, [0, 2], [256]),                   # tiles of 128 queries
     (71, 1, 64, 48, [1000, 1001, 1100], [1, 1, 2], None, [0, 3], [999]),
     (4, 2, 32, 16, [3000] * 12, [1] * 12, None, [0, 12], [2990]),               # split along the prompt
+    (16, 8, 64, 16, [70 + b % 61 for b in range(700)], [1 + (b % 9 == 4) for b in range(700)], None,    # many items a workgroup,
+     [0, 3, 400, 400, 640, 700], [64, 70, 0, 68, 0]),                                                   # a row's query a wave
 ])
 def test_attend_after_a_shared_prompt(format, dtype, heads, kv_heads, dim, page, lens, rows, width, groups, lengths):
     P = _cache(format, lens, rows, kv_heads, dim, page, TYPES[dtype], seed=dim + page)
