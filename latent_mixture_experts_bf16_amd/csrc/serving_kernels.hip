@@ -143,8 +143,21 @@ template <bool F16, int FMT, int MOST> __global__ void __launch_bounds__(MOST, M
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
             sum = sum_lanes(sum, lanes);
+            float mean = fmaf(sum, a.inv_dim, a.eps);
+            if (!(mean > 0x1p-100f && mean < __builtin_inff())) {
+                // squares that leave fp32 (of bf16 values past 2^60 or all below 2^-50): the head and the root of eps times a power of
+                // two that brings them back, which the quotient does not see; the head's lanes all come here
+                const float k = mean > 1.0f ? 0x1p-70f : 0x1p70f;
+                sum = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] *= value ? 1.0f : k;
+                    sum = fmaf(x[e], x[e], sum);
+                }
+                mean = fmaf(sum_lanes(sum, lanes), a.inv_dim, a.eps * k * k);
+            }
             if (any && !value) {
-                const float mean = fmaf(sum, a.inv_dim, a.eps), inv = mean == 0.0f ? 0.0f : rsqrtf(mean);
+                const float inv = mean == 0.0f ? 0.0f : rsqrtf(mean);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * (a.offset + w[e]);
             }

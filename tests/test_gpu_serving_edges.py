@@ -7,7 +7,7 @@ import torch
 from latent_mixture_experts_bf16_amd import binding as B
 from latent_mixture_experts_bf16_amd import drafted as D
 from latent_mixture_experts_bf16_amd import serving as S
-from test_gpu_drafted import TYPES, Paged, _attend_check, _attend_ref, _gen, _i32, _see, _starts, _trees
+from test_gpu_drafted import TINY, TYPES, Paged, _attend_check, _attend_ref, _gen, _i32, _see, _starts, _trees
 from test_gpu_serving import Mx, _cache, _means, _sample_check, _sample_ref, _share
 
 pytestmark = pytest.mark.gpu
@@ -217,6 +217,31 @@ def test_norms_of_zero_one_and_large_heads():
     y = x[:, :256].double().reshape(4, 2, 128)
     y = y / (y.square().mean(-1, keepdim=True) + 1e4).sqrt() * (1 + wide[:2].double())
     assert ((out.double().reshape(4, 2, 128) - y).abs() <= (2.0 ** -8 + 24 * 2.0 ** -24) * y.abs()).all()
+
+
+@pytest.mark.parametrize("dim", [32, 96, 256])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_norm_of_values_whose_squares_leave_fp32(dim, eps):
+    """bf16 holds values whose squares fp32 does not: the norm is that of the formula for them too."""
+    powers = [0, 59, 60, 64, 100, 124, -49, -51, -60, -100, -130]
+    n, g = len(powers), _gen(5)
+    P = Paged([0], [n], 2, dim, 16, torch.bfloat16, seed=3)
+    x = torch.randn((n, 6, dim), generator=g).clamp(-7, 7) * 2.0 ** torch.tensor(powers, dtype=torch.float64)[:, None, None]
+    x = x.to(torch.bfloat16).reshape(n, 6 * dim).cuda()
+    q, k, v = x[:, :2 * dim], x[:, 2 * dim:4 * dim], x[:, 4 * dim:]
+    w = torch.randn(dim, generator=g)
+    out = P.cache.append(D.Rope(torch.zeros(dim // 2)), q, k, v, _i32([0, n]), norm=S.HeadNorm(w.cuda(), w.cuda(), eps=eps))
+    P.cache.status()
+
+    def near(got, t):
+        t = t.double().cpu().reshape(n, 2, dim)
+        y = t / (t.square().mean(-1, keepdim=True) + float(np.float32(eps))).sqrt() * w.double()
+        tol = 24 * 2.0 ** -24 * y.abs()
+        return ((got.double().cpu().reshape(n, 2, dim) - y).abs() <= tol + 2.0 ** -8 * (y.abs() + tol) + TINY[torch.bfloat16]).all()
+
+    assert near(out, q)
+    assert near(torch.stack([P.k[P.place(0, t)] for t in range(n)]), k)
+    assert torch.equal(torch.stack([P.v[P.place(0, t)] for t in range(n)]).reshape(n, 2 * dim), v)
 
 
 # ------------------------------------------------------------------ a shared prompt
