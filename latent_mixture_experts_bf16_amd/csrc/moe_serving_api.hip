@@ -123,7 +123,8 @@ static int run_append(bool f16, int format, const moe_head_norm *norm, const App
     a.wide_weights = ((((uintptr_t)a.q_weight | (uintptr_t)a.k_weight) & 15) | ((a.qw_stride | a.kw_stride) & unit)) == 0;
     for (a.lanes = 4; a.lanes * 8 < a.r.c.dim; a.lanes *= 2) {}
     // Few rows (one to a compute unit): as many threads as their heads take, whole waves, at least as many as pairs; more rows: 256
-    // (the kernel of one row of 48 heads of 128: 4.2 us, 5.8 with 256 threads; the call of 2001 rows: 33.2 us with 768, 17.6 with 256).
+    // (the kernel of one row of 48 heads of 128: 4.2 us, 5.8 with 256 threads; the call of 2001 rows: 33.2 us with
+    // 768, 17.6 with 256, when both were measured; 18.1 since).
     const int threads = ((call.q_heads + 2 * a.r.c.heads) * a.lanes + 63) & ~63;
     const bool few = call.rows <= COMPUTE_UNITS && threads > 256;
     const int block = !few ? 256 : threads < 1024 ? threads : 1024;
