@@ -58,8 +58,8 @@ __device__ __forceinline__ RowHeat row_heat(const SampleParams &p, int row) {
 }
 
 // The grid that all logits of a row are placed on: the nearest whole number of steps, rising with the logit, the same wherever
-// it is computed. Eight steps make a cell. (1.5 2^52 added leaves the number in the low bits; from 2^50 on there are only
-// whole numbers.)
+// it is computed. Eight steps make a cell. (1.5 2^52 added leaves the number in the low bits. From 2^50 on, where that does not
+// hold, the product is taken as it is: two different logits are then millions of steps apart.)
 constexpr double ROUND = 6755399441055744.0;
 __device__ __forceinline__ double grid(float x, double steps) {
     const double near = fma((double)x, steps, ROUND) - ROUND, far = (double)x * steps;
@@ -80,27 +80,30 @@ struct Power32 {
     double c1 = 0.02166084939249829, c2 = c1 * c1 / 2.0, c3 = c1 * c1 * c1 / 6.0, c4 = c1 * c1 * c1 * c1 / 24.0,
            c5 = c1 * c1 * c1 * c1 * c1 / 120.0;     // c1: log(2) / 32
     __device__ __forceinline__ Power32() { asm("" : "+s"(c1), "+s"(c2), "+s"(c3), "+s"(c4), "+s"(c5)); }
-    __device__ __forceinline__ double operator()(int k, double r) const {
-        const double m = exp_table()[k & 31];
+    // 2^(r / 32) - 1
+    __device__ __forceinline__ double rest(double r) const {
         double e = fma(r, c5, c4);
         e = fma(e, r, c3);
         e = fma(e, r, c2);
         e = fma(e, r, c1);
-        e = fma(m, e * r, m);
+        return e * r;
+    }
+    __device__ __forceinline__ double operator()(int k, double r) const {
+        const double m = exp_table()[k & 31], e = fma(m, rest(r), m);
         return __hiloint2double(__double2hiint(e) + ((k >> 5) * (1 << 20)), __double2loint(e));
     }
 };
 __device__ __forceinline__ double power32(int k, double r) { return Power32()(k, r); }
-// Weights are in 2^(top / 32), top being the largest logit's place on the grid. Where that is infinite, all weight is
-// on it. What lies 64 octaves below weighs nothing.
-__device__ __forceinline__ double weight_of(float x, double steps, double top) {
-    if (top == __builtin_inf()) return x == __builtin_inff() ? 1.0 : 0.0;
-    const double g = grid(x, steps), d = g - top;
-    if (!(d > -2048.0)) return 0.0;
-    return power32((int)d, fabs(g) < 0x1p50 ? fma((double)x, steps, -g) : 0.0);
+// The weight of a logit x beside the largest one of its chunk or row, `top`: that one weighs exactly 1, and so does every
+// other that is equal to it, so that a border that falls exactly between two of them (top-p of one half over two equal logits)
+// falls there in these sums and quotients too. (Borders of different weights are never exact: exponentials of different
+// rational numbers have no such sums.) Where the largest is infinite, all weight is on it. What lies 64 octaves below weighs
+// nothing.
+__device__ __forceinline__ double weight_of(float x, float top, double steps) {
+    if (top == __builtin_inff()) return x == top ? 1.0 : 0.0;
+    const double t = (double)x - (double)top, d = t * steps, k = rint(d);
+    return d > -2048.0 ? power32((int)k, fma(t, steps, -k)) : 0.0;
 }
-// 2^(d / 32) of whole numbers d <= 0.
-__device__ __forceinline__ double power32_of(double d) { return d >= -2048.0 ? power32((int)d, 0.0) : 0.0; }
 // A weight of at most 2 as a whole number of 2^-50, to nearest: the low bits of its sum with 4.
 __device__ __forceinline__ uint64_t whole50(double w) {
     return (uint64_t)__double_as_longlong(fma(w, 0x1p50, 0x1p52)) & 0xFFFFFFFFFFFFFull;
@@ -175,15 +178,20 @@ template <typename L> __global__ void __launch_bounds__(256) moe_sample_cells_ke
     // additions at one place would take one after another
     const float lowest = (float)((top_g - 2304.0) / h.steps);      // what lies below weighs nothing
     const bool equal = x[0] > lowest && __ballot(x[0] == __int_as_float(uniform(__float_as_int(x[0])))) == ~0ull;
+    const Power32 power;
+    // The table of powers over the power of the largest logit's own rest on the grid: the weights below are places' on the grid, and
+    // are so beside the largest logit. Its own is then 1 to within three roundings, which is 2^50 whole numbers of 2^-50.
+    if (tid < 32) exp_table()[tid] /= 1.0 + power.rest(fma((double)top, h.steps, -top_g));
     const bool slow = __syncthreads_or(equal || !(fabs(top_g) < 0x1p29 && lowest > -__builtin_inff())) != 0;
     if (tid == 0) p.head[at] = {top_g, top, !slow};
     if (!(top > -__builtin_inff())) return;
     if (slow) {
+        fill_exp_table();
 #pragma unroll 1
         for (int i = c * SAMPLE_CHUNK + tid; i < min(p.vocab, (c + 1) * SAMPLE_CHUNK); i += 256) {
             const float v = L::value(row_of<L>(p, row)[i]);
             if (v > -__builtin_inff())
-                add_to(mass, count, cells_below(top_g, grid(v, h.steps)), whole50(weight_of(v, h.steps, top_g)), v);
+                add_to(mass, count, cells_below(top_g, grid(v, h.steps)), whole50(weight_of(v, top, h.steps)), v);
         }
         __syncthreads();
         p.mass[at * SAMPLE_CELLS + tid] = mass[tid];
@@ -194,7 +202,6 @@ template <typename L> __global__ void __launch_bounds__(256) moe_sample_cells_ke
     // below, or is a NaN, is taken to the last cell, where a weight is nothing in 2^-50.
     uint32_t place[SHARE], last_n = 0;
     const int top_n = (int)top_g, top_d = top_n >> 3;
-    const Power32 power;
 #pragma unroll
     for (int k = 0; k < SHARE; ++k) {
         const double v = (double)fmaxf(x[k], lowest), t = fma(v, h.steps, ROUND);
@@ -289,11 +296,13 @@ template <typename L> struct Row {
     RowLds &s;
     const typename L::T *logits;
     double steps, top_g;
+    float top;
     bool in_list;
 
-    __device__ __forceinline__ double weight(uint32_t key) const { return weight_of(value_of<L>(key), steps, top_g); }
+    __device__ __forceinline__ double weight(uint32_t key) const { return weight_of(value_of<L>(key), top, steps); }
     __device__ __forceinline__ int cell(float x) const { return cells_below(top_g, grid(x, steps)); }
-    // Weights of cell c are below 2^((1 - c) / 4 + 1 / 64), so that whole numbers of 2^-shift add up in 64 bits.
+    // Weights of cell c are below 2^((1 - c) / 4 + 1 / 32), so that whole numbers of 2^-shift, the weight of at most 2^(32 - clz)
+    // logits, add up in 64 bits (below 2^61.3).
     __device__ __forceinline__ int shift_of(int c) const {
         return c / 4 + 29 + __builtin_clz(max(s.upto_count[c + 1] - s.upto_count[c], 1u));
     }
@@ -622,7 +631,7 @@ template <typename L> __global__ void __launch_bounds__(ROW_THREADS) moe_sample_
     if (tid < p.chunks) {
         const bool some = head.top > -__builtin_inff();
         s.below[tid] = some ? cells_below(top_g, head.top_g) : -1;
-        s.factor[tid] = !some ? 0.0 : head.top_g == top_g ? power2(-50) : power32_of(head.top_g - top_g) * power2(-50);
+        s.factor[tid] = some ? weight_of(head.top, top, h.steps) * power2(-50) : 0.0;
     }
     // whether the chunks of the row listed their logits
     const bool listed = !__syncthreads_or(!head.listed && head.top > -__builtin_inff());
@@ -668,8 +677,8 @@ template <typename L> __global__ void __launch_bounds__(ROW_THREADS) moe_sample_
     __syncthreads();
     enum { K, P, M, D };
     const uint32_t k = h.greedy ? 1u : asked_k > 0 ? (uint32_t)asked_k : 0xFFFFFFFFu;
-    const double least_weight = (double)min_p * weight_of(top, h.steps, top_g);
-    Row<L> r = {p, s, row_of<L>(p, row), h.steps, top_g, true};
+    const double least_weight = (double)min_p;
+    Row<L> r = {p, s, row_of<L>(p, row), h.steps, top_g, top, true};
     // what has to be reached, where `left` is left by the cuts before: the draw passes its part of that, and so reaches the next number
     auto goal_of = [&](int i, double left) {
         return i == K ? (double)k : i == P ? (double)top_p * left
@@ -731,7 +740,7 @@ template <typename L> __global__ void __launch_bounds__(ROW_THREADS) moe_sample_
             Span c;
             if (i == M) {
                 // the logarithm in 32 bits is within 1/100 of a step
-                const double g = top_g + (double)(32.0f * __log2f((float)least_weight));
+                const double g = (double)top * h.steps + (double)(32.0f * __log2f((float)least_weight));
                 c = {max(cells_below(top_g, g + 0.75), 0), cells_below(top_g, g - 0.75)};
                 if (top_g == __builtin_inf()) c = {0, 0};
             } else {
