@@ -833,7 +833,7 @@ __global__ void __launch_bounds__(256, 8) moe_shared_join_kernel(SharedJoinParam
     __shared__ f32x4 so[4][U];
     const int lane = lane_id(), wave = uniform((int)threadIdx.x >> 6);
     const bool apart = p.apart != 0;       // a workgroup for each query
-    const int64_t query = apart ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
+    const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, query = apart ? block : block * 4 + wave;
     const int row = uniform((int)divide(query, p.q_heads)), head = uniform((int)(query - (int64_t)row * p.q_heads));
     if (row >= p.rows) return;
     int first = 0;

@@ -191,7 +191,9 @@ int attend_run(const AttendCall &a, AttendParams &p) {
     // they save (4096: 109 and 106 us; 8192 of 256 short sequences: 67 and 57).
     const int64_t queries = (int64_t)p.rows * p.q_heads;
     j.apart = queries < 8 * COMPUTE_UNITS;
-    return launch("shared join", k.shared_join, dim3((unsigned)(j.apart ? queries : (queries + 3) / 4)), dim3(256), j, a.stream);
+    // a grid's x holds less than 2^32 threads (past that a launch wrapped, without an error): more workgroups go on along y
+    const int64_t blocks = j.apart ? queries : (queries + 3) / 4, x = blocks < 1 << 20 ? blocks : 1 << 20;
+    return launch("shared join", k.shared_join, dim3((unsigned)x, (unsigned)((blocks + x - 1) / x)), dim3(256), j, a.stream);
 }
 
 }  // namespace moe
