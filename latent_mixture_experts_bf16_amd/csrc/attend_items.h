@@ -268,6 +268,11 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
     constexpr int SPREAD = 2 * D / ROW;                        // 16-byte pieces in LDS that one loaded piece becomes
     constexpr bool RAGGED = PIECES % 64 != 0;
     constexpr int GE = 16 * D;                                 // elements of a group of 16 tokens
+    // Whether the pages of 64 tiles are looked up at once, or that of one (16 bits): where the two registers that it takes go to
+    // scratch it costs more than it gives (the whole call, one and 64: widths 96 and 256, 128 queries a tile, 8 x 16 rows over 4100
+    // tokens 51.1 and 52.4 us, 70.1 and 74.3; width 80 54.9 and 53.6; width 256, 64 queries, 8 x 7 rows over 8200 76.2 and 71.4;
+    // width 128, 64 queries, 8 trees of 16 over up to 8200 54.6 and 54.0).
+    constexpr bool AHEAD = FMT != MX_NONE || MQ < 128 || (D != 96 && D != 256);
     __shared__ __align__(16) uint16_t lds[2][2][4 * GE];
     __shared__ float sm[4][16 * NQ], sl[4][16 * NQ];
     __shared__ __align__(16) int note[2][4];                   // per buffer and group: 1 page bad, 2 V not finite
@@ -285,15 +290,17 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
 
     // this lane's pieces of a group of 16 tokens: where they come from and where they go
     uint32_t ko[LOADS], vo[LOADS], kso[LOADS], vso[LOADS];     // the latter: of the scales
-    int pt[LOADS], pc[LOADS];
+    int pt[LOADS], pc[LOADS], kp[LOADS], vp[LOADS];
 #pragma unroll
     for (int k = 0; k < LOADS; ++k) {
         const int at = min(k * 64 + lane, PIECES - 1), t = at / (ROW / 16), c = at % (ROW / 16);
         constexpr int UNIT = FMT == MX_NONE ? 2 : 1;           // bytes that strides count
         pt[k] = t;
         pc[k] = c * SPREAD;
-        ko[k] = (uint32_t)(t * p.c.k.slot * UNIT + c * 16);
-        vo[k] = (uint32_t)(t * p.c.v.slot * UNIT + c * 16);
+        kp[k] = wave * GE + k_place<D>(t, c * SPREAD);
+        vp[k] = wave * GE + v_unit<D>(t, c * SPREAD >> 1) + (c * SPREAD & 1) * 8;
+        ko[k] = (uint32_t)(t * p.c.k.slot + c * (16 / UNIT)) * UNIT;
+        vo[k] = (uint32_t)(t * p.c.v.slot + c * (16 / UNIT)) * UNIT;
         if (FMT != MX_NONE) {
             kso[k] = (uint32_t)(t * p.c.ks.slot + c * SPREAD / 4);
             vso[k] = (uint32_t)(t * p.c.vs.slot + c * SPREAD / 4);
@@ -328,12 +335,12 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
 
         const int32_t *table = p.c.table + (SHARED ? uniform(sq.seq) : b) * p.c.table_stride;
         // The pages of this wave's group of 64 tiles, a lane each, looked up 64 tiles before they are needed: loads come back in
-        // their order, and a look-up for each tile would have to wait for the tile before it.
+        // their order, and a look-up for each tile has to wait for the tile before it. (Else the page of one tile.)
         auto pages_of = [&](int tile) {
-            const int64_t t = ((int64_t)tile + lane) * 64 + wave * 16;      // a tile past the last may lie past 2^31
+            const int64_t t = ((int64_t)tile + (AHEAD ? lane : 0)) * 64 + wave * 16;      // a tile past the last may lie past 2^31
             return t < end ? table[(int)t / p.c.page] : -1;
         };
-        int pages_from = first_tile, pages = pages_of(first_tile), pages_next = pages_of(first_tile + 64);
+        int pages_from = first_tile, pages = AHEAD ? pages_of(first_tile) : 0, pages_next = AHEAD ? pages_of(first_tile + 64) : 0;
 
         s16x8 qf[NQ][KS];
         uint64_t mask[NQ];
@@ -401,51 +408,75 @@ __global__ void __launch_bounds__(256, attend_blocks(D, 16 * NQ * QW)) moe_atten
         };
 
         bool good = true;
-        if (first_tile < t_last) good = load(first_tile, page_of(first_tile));
+        if (AHEAD) {
+            if (first_tile < t_last) good = load(first_tile, page_of(first_tile));
+        } else if (first_tile < t_last) {
+            good = load(first_tile, uniform(pages_of(first_tile)));
+            pages = pages_of(first_tile + 1);
+        }
         for (int tile = first_tile; tile < t_last; ++tile) {
             const int buf = tile & 1, t0 = tile * 64;
             uint16_t *const kl = lds[buf][0], *const vl = lds[buf][1];
             int told = good ? 0 : 1;
-            // what a loaded piece stands for, in 16 bits
-            u32x4 vx[LOADS][SPREAD];
+            // the step's own tokens: slots behind the last hold anything, and are zeroed; a value that is not finite must not
+            // reach the rows that do not see it. (Cleaned in place in 16 bits: a copy of the values spilled, 53 us in place
+            // of 47 for width 256 and 64 queries a tile.)
+            const bool clean = t0 + wave * 16 + 16 > len || !good;
+            auto cleaned = [&](int k, u32x4 &v) {
+                const int t = t0 + wave * 16 + pt[k];
+                if (t >= end || !good) v = u32x4{0, 0, 0, 0};
+                return (int)(t >= len) & (odd2<F16>(v.x) | odd2<F16>(v.y) | odd2<F16>(v.z) | odd2<F16>(v.w));
+            };
+            int odd = 0;
+            if constexpr (FMT == MX_NONE) {
+                if (clean) {
 #pragma unroll
-            for (int k = 0; k < LOADS; ++k) {
-                u32x4 kx[SPREAD];
-                mx_expand<F16, FMT>(kr[k], ksr[k], kx);
-                if (!RAGGED || k * 64 + lane < PIECES) {
-#pragma unroll
-                    for (int s = 0; s < SPREAD; ++s)
-                        *(u32x4 *)(kl + wave * GE + k_place<D>(pt[k], pc[k] + s)) = kx[s];
+                    for (int k = 0; k < LOADS; ++k) odd |= cleaned(k, vr[k]);
+                    if (__any(odd)) told |= 2;
                 }
-            }
-#pragma unroll
-            for (int k = 0; k < LOADS; ++k) mx_expand<F16, FMT>(vr[k], vsr[k], vx[k]);
-            if (t0 + wave * 16 + 16 > len || !good) {
-                // the step's own tokens: slots behind the last hold anything, and are zeroed; a value that is not finite
-                // must not reach the rows that do not see it
-                int odd = 0;
 #pragma unroll
                 for (int k = 0; k < LOADS; ++k)
-#pragma unroll
-                    for (int s = 0; s < SPREAD; ++s) {
-                        const int t = t0 + wave * 16 + pt[k];
-                        u32x4 &v = vx[k][s];
-                        if (t >= end || !good) v = u32x4{0, 0, 0, 0};
-                        odd |= (int)(t >= len) & (odd2<F16>(v.x) | odd2<F16>(v.y) | odd2<F16>(v.z) | odd2<F16>(v.w));
+                    if (!RAGGED || k * 64 + lane < PIECES) {
+                        *(u32x4 *)(kl + kp[k]) = kr[k];
+                        *(u32x4 *)(vl + vp[k]) = vr[k];
                     }
-                if (__any(odd)) told |= 2;
-            }
+            } else {
+                // what a loaded piece stands for, in 16 bits
+                u32x4 vx[LOADS][SPREAD];
 #pragma unroll
-            for (int k = 0; k < LOADS; ++k)
-                if (!RAGGED || k * 64 + lane < PIECES) {
+                for (int k = 0; k < LOADS; ++k) {
+                    u32x4 kx[SPREAD];
+                    mx_expand<F16, FMT>(kr[k], ksr[k], kx);
+                    if (!RAGGED || k * 64 + lane < PIECES) {
 #pragma unroll
-                    for (int s = 0; s < SPREAD; ++s) {
-                        const int c = pc[k] + s;
-                        *(u32x4 *)(vl + wave * GE + v_unit<D>(pt[k], c >> 1) + (c & 1) * 8) = vx[k][s];
+                        for (int s = 0; s < SPREAD; ++s)
+                            *(u32x4 *)(kl + wave * GE + k_place<D>(pt[k], pc[k] + s)) = kx[s];
                     }
                 }
+#pragma unroll
+                for (int k = 0; k < LOADS; ++k) mx_expand<F16, FMT>(vr[k], vsr[k], vx[k]);
+                if (clean) {
+#pragma unroll
+                    for (int k = 0; k < LOADS; ++k)
+#pragma unroll
+                        for (int s = 0; s < SPREAD; ++s) odd |= cleaned(k, vx[k][s]);
+                    if (__any(odd)) told |= 2;
+                }
+#pragma unroll
+                for (int k = 0; k < LOADS; ++k)
+                    if (!RAGGED || k * 64 + lane < PIECES) {
+#pragma unroll
+                        for (int s = 0; s < SPREAD; ++s) {
+                            const int c = pc[k] + s;
+                            *(u32x4 *)(vl + wave * GE + v_unit<D>(pt[k], c >> 1) + (c & 1) * 8) = vx[k][s];
+                        }
+                    }
+            }
             if (lane == 0) note[buf][wave] = told;
-            if (tile + 1 < t_last) good = load(tile + 1, page_of(tile + 1));
+            if (tile + 1 < t_last) {
+                good = load(tile + 1, AHEAD ? page_of(tile + 1) : uniform(pages));
+                if (!AHEAD) pages = pages_of(tile + 2);
+            }
             __syncthreads();
             const int4 notes = *(const int4 *)note[buf];
             const int all = uniform(notes.x | notes.y << 4 | notes.z << 8 | notes.w << 12);   // four bits a group
