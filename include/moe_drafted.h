@@ -75,7 +75,8 @@ typedef struct {
 /* Rotate the step's queries into q_out and its keys into the cache, and copy its values there:
  * row i of sequence b becomes cached token len[b] + i (len itself does not change).
  *   q [rows][q_heads * dim], k and v [rows][kv_heads * dim] in the cache's type, rows at the
- *     given strides (elements); heads side by side. Any alignment of 2 bytes (16 is fastest).
+ *     given strides (elements); heads side by side. Any alignment of 2 bytes (16 is fastest);
+ *     interleaved pairs need 4.
  *   positions  [rows] i32, or NULL: row i of sequence b is at len[b] + i
  *   q_out      [rows][q_heads * dim]; may be q itself (same pointer and stride), no other overlap
  * The angle is formed in 64 bits, so far positions lose nothing. Rows that row_start gives to no

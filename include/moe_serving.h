@@ -114,9 +114,12 @@ int moe_mx_keep(const moe_mx_cache *c, const int32_t *row_start, int32_t rows, c
  *   top-p: the shortest beginning whose weight reaches top_p times that of the first top_k (1 or more: no cut; one token is left always);
  *   min-p: those with w_i >= min_p (0 or less: no cut; above 1 it counts as 1),
  * whichever leaves the fewest. The token is the first in that order whose running weight passes u times that of all that are left.
- * T <= 0: the largest logit's lowest index, and logprob 0. Weights are held in 64 bits (2^-50 of a part's largest one
- * where they are added in an order that varies, so that the same inputs always give the same token). NaN logits count as
- * -infinity, which is never drawn; a row without a value above that gives token 0 and sets MOE_FLAG_LOGITS. NaN in top_p, min_p: no cut; in T: as 0; u is taken into [0, 1).
+ * T <= 0: the largest logit's lowest index, and logprob 0. Weights are held in 64 bits, the largest
+ * logit's as exactly 1, so that a border exactly between logits equal to it lies there. Where weights are added in an order that
+ * varies, they are whole numbers of a unit, and the same inputs always give the same token: the unit is 2^-50 of the largest weight of
+ * 4096 neighbouring logits; where a border is looked for among n logits within a quarter octave of weight, 2^-39 of theirs
+ * or less (n up to 2^20; 2^-49 for 2000). NaN logits count as -infinity, which is never drawn; a row without a value above that
+ * gives token 0 and sets MOE_FLAG_LOGITS. NaN in top_p, min_p: no cut; in T: as 0; u is taken into [0, 1).
  *   logits       [rows][vocab] f32, bf16 or f16, rows at any stride >= vocab; vocab 1 .. 2^20
  *   u            [rows] f32
  *   temperature, top_p, min_p  [rows] f32, top_k [rows] i32; each may be NULL: 1, and no cut

@@ -106,7 +106,7 @@ __device__ __forceinline__ double *exp_table() {
     __shared__ double t[32];
     return t;
 }
-// Every kernel below calls this first, with all its threads.
+// A kernel that takes exponentials calls this before the first of them, with all its threads.
 __device__ __forceinline__ void fill_exp_table() {
     if (threadIdx.x < 32) exp_table()[threadIdx.x] = EXP2_TABLE[threadIdx.x];
     __syncthreads();

@@ -2,7 +2,7 @@
 //
 // 32 values along a head share a byte e, which stands for 2^(e - 127) (255: NaN); a value is a code, e4m3 or e2m1, times that.
 // The conversions below are the CDNA4 instructions for exactly these formats: powers of two change no digit, so what
-// they give is exact in bf16, and in f16 down to its smallest number.
+// they give is exact wherever the type has the number, else rounded once (next to its smallest number, and infinite past its largest one).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>

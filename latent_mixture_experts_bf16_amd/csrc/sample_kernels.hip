@@ -5,7 +5,8 @@
 // the cells of a grid of a quarter of an octave of weight (a workgroup per chunk, whole card), and one workgroup per
 // row finds the cells that matter and looks at their logits alone, narrowing to one value in steps of 10 bits of its
 // ordered bits. Whole tokens come out, so weights and sums are in 64 bits. Where atomics add in an order that varies, they add
-// whole numbers (the weight in 2^-50 of the largest one), so that the same inputs always give the same token.
+// whole numbers, so that the same inputs always give the same token: weights in 2^-50 of their chunk's largest one, and within a
+// cell in the least unit that its number of logits leaves room for in 64 bits (Row::shift_of).
 #include <type_traits>
 
 #include "logit_items.h"
@@ -145,10 +146,10 @@ __device__ __forceinline__ void add_to(uint64_t *mass, uint32_t *count, int at, 
 // Besides counts and weights, the chunk's logits but those of its last cell are listed by cell (their numbers within the chunk), so that
 // the row's workgroup reads only those of the cells that matter: a pass over the row by one workgroup takes 11 us and more.
 //
-// Bound by LDS atomics (one of 64 bits and one of 32 a logit; the former some 20 us of the 45) and the vector instructions of the
-// weight: 256 rows of 100003 fp32 logits, 102 MB, 45 us; 64 rows of 131072 bf16 logits 20 us; one row, whose 32 workgroups leave
-// most of the card idle, 7.4 us. Three atomics of 32 bits in place of the one of 64 took 55 us, a form without branches, which
-// holds 107 registers, 50 (this one 47 then).
+// Bound by LDS atomics (one of 64 bits and one of 32 a logit; the former some 20 us of the 47) and the vector instructions of the
+// weight (three quarters of the time): 256 rows of 100003 fp32 logits, 102 MB, 47 us; 64 rows of 131072 bf16 logits 21 us; one
+// row, whose 32 workgroups leave most of the card idle, 7.4 us. Three atomics of 32 bits in place of the one of 64 took 55 us, a
+// form without branches, which holds 107 registers, 50 (this one 47 then).
 template <typename L> __global__ void __launch_bounds__(256) moe_sample_cells_kernel(SampleParams p) {
     __shared__ uint64_t mass[SAMPLE_CELLS];
     __shared__ uint32_t count[SAMPLE_CELLS];
@@ -602,7 +603,7 @@ template <typename L> struct Row {
 
 // Bound by its chains: loads of the chunks' heads and cells (5 us), the cells' decisions by one wave (4 us), lists and then values of
 // the cells that matter and the steps through their bits (4 to 20 us), and the fetch of its instructions: one row 20 us, 64
-// rows of bf16 logits with all cuts 35, 256 rows 39. With 256 threads the last took 65 us.
+// rows of bf16 logits with all cuts 34, 256 rows 38. With 256 threads the last took 65 us.
 template <typename L> __global__ void __launch_bounds__(ROW_THREADS) moe_sample_row_kernel(SampleParams p) {
     __shared__ RowLds s;
     const int row = (int)blockIdx.x, tid = (int)threadIdx.x, lane = lane_id(), wave = uniform(tid >> 6);

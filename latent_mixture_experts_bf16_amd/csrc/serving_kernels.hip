@@ -77,9 +77,10 @@ __device__ __forceinline__ uint4 load_head(const uint16_t *q, int64_t q_row, int
 //
 // A pass's loads are on the way before the pass before it is computed, the first ones before the row's sequence, page and angles are
 // found: what bounds a call of few rows is that chain of loads (the kernel of one row: 4.4 us). MOST threads: of few rows all heads at
-// once (1024), of many 256, eight of whose workgroups a compute unit holds: those are bound by vector instructions (2001 rows of
-// 56 heads of 128, 57 MB: 18 us, of which the floor of bytes is 12; 2808 rows to 4-bit codes: 19 us; before sums went by
-// data-parallel moves, roundings by pairs and the loads ahead, the former took 28).
+// once (1024), of many 256, six of whose workgroups a compute unit holds (80 registers, and 24 bytes of scratch a lane in 16 bits,
+// 40 and 48 to codes): vector instructions take 62 % of those' time (2001 rows of 56 heads of 128, 57 MB: 18 us, of which the floor
+// of bytes is 12) and 57 % (2808 rows to 4-bit codes: 19 us), and the rows past the first 1536 wait for a place. Before sums went by
+// data-parallel moves, roundings by pairs and the loads ahead, the former took 28.
 template <bool F16, int FMT, int MOST> __global__ void __launch_bounds__(MOST, MOST > 256 ? 1 : 6) moe_append_kernel(AppendParams a) {
     __shared__ __align__(16) float2 cs[128];
     __shared__ __align__(16) float xs[MOST * 8];
